@@ -51,9 +51,16 @@ class csa2_decode_args(ctypes.Structure):
                 ("idx", c_void_p), ("pool", c_void_p), ("o", c_void_p), ("lse", c_void_p)]
 
 
+class csa2_rotary(ctypes.Structure):
+    _fields_ = [("step", c_void_p), ("rot_dim", c_int32), ("first", c_int32), ("layout", c_int32), ("scale", c_float)]
+
+
 LAYER_SWA = 4
+ROTARY_LAYOUT = {"interleaved": 0, "half": 1}
+ROTARY_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 _P = ctypes.POINTER(csa2_cache)
 _PD = ctypes.POINTER(csa2_decode_args)
+_PR = ctypes.POINTER(csa2_rotary)
 _SIGS = {
     "csa2_version": ([], ctypes.c_int),
     "csa2_last_error_string": ([], ctypes.c_char_p),
@@ -88,6 +95,20 @@ _SIGS = {
                            c_void_p, c_void_p], ctypes.c_int),
     "csa2_decode_workspace_size": ([_PD], c_size_t),
     "csa2_decode_step": ([_PD, c_void_p, c_size_t, c_void_p, c_void_p], ctypes.c_int),
+    "csa2_rotary_table": ([c_int32, ctypes.c_double, ctypes.c_int, ctypes.c_double, c_int32, ctypes.c_double,
+                           ctypes.c_double, c_void_p, c_void_p], ctypes.c_int),
+    "csa2_rotate": ([c_void_p, ctypes.c_int, c_int64, c_int64, c_void_p, ctypes.c_int, c_int64, c_int64, c_int32,
+                     c_int32, c_int32, c_void_p, _PR, c_int32, c_void_p], ctypes.c_int),
+    "csa2_pack_kv_rotary": ([c_void_p, c_void_p, ctypes.c_int, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_void_p,
+                             _PR, _PR, _P, c_void_p, c_void_p, c_void_p, c_void_p], ctypes.c_int),
+    "csa2_append_kv_rotary": ([c_void_p, c_void_p, ctypes.c_int, c_int32, c_void_p, c_void_p, _PR, _PR, _P, c_void_p,
+                               c_void_p, c_void_p, c_void_p], ctypes.c_int),
+    "csa2_pack_swa_rotary": ([c_void_p, ctypes.c_int, c_int32, c_int32, c_void_p, _PR, c_void_p, c_void_p, c_int32,
+                              c_void_p, c_void_p], ctypes.c_int),
+    "csa2_prefix_workspace_size": ([c_int32, c_int32, c_int32], c_size_t),
+    "csa2_prefix_attn": ([c_void_p, c_int32, c_int32, c_void_p, c_float, c_int32, c_int32, _P, c_void_p, c_void_p,
+                          c_int32, c_int32, c_void_p, ctypes.c_int, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p],
+                         ctypes.c_int),
 }
 for _name, (_args, _ret) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -363,3 +384,183 @@ class DecodeStep:
     def run(self, ws, err=None, stream=None):
         _ok(_lib.csa2_decode_step(ctypes.byref(self.args), _ptr(ws), 0 if ws is None else ws.numel(), _ptr(err),
                                   _stream(stream)), "csa2_decode_step")
+
+
+def csa2_rotary_table(rot_dim, base=10000.0, scaling="none", factor=1.0, original_len=0, beta_fast=32.0, beta_slow=1.0):
+    """Steps (2^64ths of a turn per position, int64 bits of a uint64) of rot_dim / 2 pairs, on the host, and the
+    attention scale that goes with the scaling."""
+    step = torch.empty(max(rot_dim // 2, 0), dtype=torch.int64)
+    scale = c_float()
+    _ok(_lib.csa2_rotary_table(rot_dim, base, ROTARY_SCALING[scaling], factor, original_len, beta_fast, beta_slow,
+                               step.data_ptr() or None, ctypes.addressof(scale)), "csa2_rotary_table")
+    return step, scale.value
+
+
+class Rotary:
+    """A rotation of 2 * len(step) dims of a head, from dim `first`: its device table of steps and descriptor.
+
+    Rotary.table(64, ..., device=..., first=448, layout="half") makes the steps with csa2_rotary_table.
+    """
+
+    def __init__(self, step, first=0, layout="interleaved", scale=1.0):
+        if step.dtype != torch.int64 or step.dim() != 1:
+            raise ValueError("step must be a one-dimensional int64 tensor")
+        self.step, self.first, self.layout, self.scale = step, int(first), layout, float(scale)
+        d = csa2_rotary()
+        if layout not in ROTARY_LAYOUT:
+            raise ValueError(f"layout must be one of {sorted(ROTARY_LAYOUT)}")
+        d.step, d.rot_dim, d.first = _ptr(step), 2 * step.numel(), self.first
+        d.layout, d.scale = ROTARY_LAYOUT[layout], self.scale
+        self._desc = d
+
+    @classmethod
+    def table(cls, rot_dim, first=0, layout="interleaved", device="cuda", **scaling):
+        step, scale = csa2_rotary_table(rot_dim, **scaling)
+        return cls(step.to(device), first, layout, scale)
+
+    def desc(self):
+        return self._desc
+
+
+def _rot(r):
+    return None if r is None else ctypes.byref(r.desc())
+
+
+def _on(device, stream, *tensors):
+    """The stream of a call whose tensors are all on `device` (None is no tensor), which must be the current one."""
+    if device.type != "cuda":
+        raise ValueError("CSA2 tensors must live on a CUDA device")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("the tensors of a CSA2 call must be on one device")
+    if device.index != torch.cuda.current_device():
+        raise ValueError("the tensors of a CSA2 call must be on the current device")
+    return _stream(stream)
+
+
+def _shape(t, shape, dtype, what):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{what} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+
+
+def csa2_rotate(x, pos, rotary, inverse=False, out=None, out_dtype=None, stream=None):
+    """Rotary positions of x [..., heads, dim] at positions pos [...] (inverse: turned back).
+
+    The token dims of x may be strided as long as they form one stride; out (default: a new tensor of out_dtype or
+    x's type) may be x itself.  Tokens at negative positions are padding: their rows of out are left as they are.
+    """
+    if x.dim() < 2 or tuple(pos.shape) != tuple(x.shape[:-2]) or pos.dtype != torch.int32:
+        raise ValueError("pos must be int32 and shaped like x without its last two dims")
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    elif out.shape != x.shape:
+        raise ValueError("out must be shaped like x")
+    s = _on(x.device, stream, x, pos, out, rotary.step)
+    if x.dtype not in DTYPE or out.dtype not in DTYPE:
+        raise ValueError("x and out must be float32 or bfloat16")
+    heads, dim = x.shape[-2:]
+    (xt, xh), (ot, oh) = _head_strides(x, "x"), _head_strides(out, "out")
+    _ok(_lib.csa2_rotate(x.data_ptr(), DTYPE[x.dtype], xt, xh, out.data_ptr(), DTYPE[out.dtype], ot, oh, pos.numel(),
+                         heads, dim, _ptr(pos), _rot(rotary), int(inverse), s), "csa2_rotate")
+    return out
+
+
+def _head_strides(t, what):
+    """(token stride, head stride) of [..., heads, dim]; the token dims must form one stride."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what} must have unit stride along dim")
+    token = None
+    for n, st in reversed(list(zip(t.shape[:-2], t.stride()[:-2]))):
+        if n == 1:
+            continue
+        if token is None:
+            token, span = st, st * n
+        elif st != span:
+            raise ValueError(f"the token dims of {what} must form one stride")
+        else:
+            span = st * n
+    return token or 0, t.stride(-2) if t.shape[-2] > 1 else 0
+
+
+def csa2_pack_kv_rotary(lat_kv, lat_ix, first_entry, cache, rot_kv, rot_ix, pool_w=None, gate_kv=None, gate_ix=None,
+                        kv_hat=None, ix_hat=None, err=None, stream=None):
+    """csa2_pack_kv / csa2_pack_kv_gated with entries turned at their positions (rot_kv / rot_ix: Rotary or None).
+    kv_hat [B][T // r][512], ix_hat [B][T // r][128] bf16 (optional) receive the values that the codes stand for."""
+    B, T = lat_kv.shape[0], lat_kv.shape[1]
+    _shape(lat_kv, (B, T, MAIN_DIM), lat_kv.dtype, "lat_kv")
+    _shape(lat_ix, (B, T, IX_DIM), lat_kv.dtype, "lat_ix")
+    _shape(first_entry, (B,), torch.int32, "first_entry")
+    _shape(pool_w, (B, T), torch.float32, "pool_w")
+    _shape(gate_kv, (B, T, MAIN_DIM), torch.float32, "gate_kv")
+    _shape(gate_ix, (B, T, IX_DIM), torch.float32, "gate_ix")
+    n = T // cache.ratio
+    _shape(kv_hat, (B, n, MAIN_DIM), torch.bfloat16, "kv_hat")
+    _shape(ix_hat, (B, n, IX_DIM), torch.bfloat16, "ix_hat")
+    s = _on(lat_kv.device, stream, lat_ix, first_entry, cache.kv_codes, pool_w, gate_kv, gate_ix, kv_hat, ix_hat, err)
+    d = cache.desc()
+    _ok(_lib.csa2_pack_kv_rotary(_ptr(lat_kv), _ptr(lat_ix), DTYPE[lat_kv.dtype], _ptr(pool_w), _ptr(gate_kv),
+                                 _ptr(gate_ix), B, T, _ptr(first_entry), _rot(rot_kv), _rot(rot_ix), ctypes.byref(d),
+                                 _ptr(kv_hat), _ptr(ix_hat), _ptr(err), s), "csa2_pack_kv_rotary")
+
+
+def csa2_append_kv_rotary(lat_kv, lat_ix, pos, cache, rot_kv, rot_ix, stage=None, kv_hat=None, ix_hat=None, err=None,
+                          stream=None):
+    """csa2_append_kv of one token per sequence (lat_kv [B][512], lat_ix [B][128]) with completed entries turned at
+    their positions; kv_hat [B][512], ix_hat [B][128] bf16 (optional) receive the completed entries' values."""
+    B = lat_kv.shape[0]
+    _shape(lat_kv, (B, MAIN_DIM), lat_kv.dtype, "lat_kv")
+    _shape(lat_ix, (B, IX_DIM), lat_kv.dtype, "lat_ix")
+    _shape(pos, (B,), torch.int32, "pos")
+    _shape(stage, (B, cache.ratio, MAIN_DIM + IX_DIM), torch.float32, "stage")
+    _shape(kv_hat, (B, MAIN_DIM), torch.bfloat16, "kv_hat")
+    _shape(ix_hat, (B, IX_DIM), torch.bfloat16, "ix_hat")
+    s = _on(lat_kv.device, stream, lat_ix, pos, cache.kv_codes, stage, kv_hat, ix_hat, err)
+    d = cache.desc()
+    _ok(_lib.csa2_append_kv_rotary(_ptr(lat_kv), _ptr(lat_ix), DTYPE[lat_kv.dtype], B, _ptr(pos), _ptr(stage),
+                                   _rot(rot_kv), _rot(rot_ix), ctypes.byref(d), _ptr(kv_hat), _ptr(ix_hat), _ptr(err),
+                                   s), "csa2_append_kv_rotary")
+
+
+def csa2_pack_swa_rotary(x, pos, swa_codes, swa_scale, rotary, err=None, stream=None):
+    """csa2_pack_swa of tokens turned at their own positions (rotary: Rotary over the 512 values)."""
+    B, T = x.shape[0], x.shape[1]
+    R = swa_codes.shape[1]
+    _shape(x, (B, T, MAIN_DIM), x.dtype, "x")
+    _shape(pos, (B, T), torch.int32, "pos")
+    _shape(swa_codes, (B, R, MAIN_DIM), torch.uint8, "swa_codes")
+    _shape(swa_scale, (B, R), torch.float32, "swa_scale")
+    s = _on(x.device, stream, pos, swa_codes, swa_scale, rotary.step, err)
+    _ok(_lib.csa2_pack_swa_rotary(_ptr(x), DTYPE[x.dtype], B, T, _ptr(pos), _rot(rotary), _ptr(swa_codes),
+                                  _ptr(swa_scale), R, _ptr(err), s), "csa2_pack_swa_rotary")
+
+
+def csa2_prefix_workspace_size(B, Q, max_entries):
+    return _lib.csa2_prefix_workspace_size(B, Q, max_entries)
+
+
+def csa2_prefix_attn(q, q_pos, cache, softmax_scale, max_entries, prefix_entries, swa_codes=None, swa_scale=None,
+                     window=128, o=None, o_dtype=torch.float32, lse=None, ws=None, err=None, stream=None):
+    """Dense attention of q [B][Q][64][512] over entries whose first prefix_entries are sequence 0's for every
+    sequence, joined with the SWA window if swa_codes / swa_scale are given.  Returns (o, lse)."""
+    B, Q = q.shape[0], q.shape[1]
+    _shape(q, (B, Q, HEADS, MAIN_DIM), torch.bfloat16, "q")
+    _shape(q_pos, (B, Q), torch.int32, "q_pos")
+    if o is None:
+        o = torch.empty((B, Q, HEADS, MAIN_DIM), dtype=o_dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, Q, HEADS), dtype=torch.float32, device=q.device)
+    if ws is None:
+        ws = torch.empty(max(csa2_prefix_workspace_size(B, Q, max_entries), 1), dtype=torch.uint8, device=q.device)
+    _shape(o, (B, Q, HEADS, MAIN_DIM), o.dtype, "o")
+    _shape(lse, (B, Q, HEADS), torch.float32, "lse")
+    R = 0
+    if swa_codes is not None:
+        R = swa_codes.shape[1]
+        _shape(swa_codes, (B, R, MAIN_DIM), torch.uint8, "swa_codes")
+        _shape(swa_scale, (B, R), torch.float32, "swa_scale")
+    s = _on(q.device, stream, q_pos, cache.kv_codes, swa_codes, swa_scale, o, lse, ws, err)
+    d = cache.desc()
+    _ok(_lib.csa2_prefix_attn(_ptr(q), B, Q, _ptr(q_pos), softmax_scale, prefix_entries, max_entries, ctypes.byref(d),
+                              _ptr(swa_codes), _ptr(swa_scale), R, window, _ptr(o), DTYPE[o.dtype], _ptr(lse),
+                              _ptr(ws), ws.numel() * ws.element_size(), _ptr(err), s), "csa2_prefix_attn")
+    return o, lse

@@ -293,3 +293,178 @@ CSA2_EXPORT csa2_status csa2_merge(const float *o1, const float *l1, const float
   csa2::launch_merge(o1, l1, o2, l2, rows, D, o, lse, stream);
   return launched("csa2_merge");
 }
+
+// ---------------------------------------------------------------- rotary positions
+namespace {
+
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7) == 0; }
+bool is_dtype(csa2_dtype t) { return t == CSA2_F32 || t == CSA2_BF16; }
+
+// A rotation of heads (or values) of `dim` dims.
+csa2_status check_rotary(const csa2_rotary *r, int dim) {
+  if (!r->step || !aligned8(r->step)) return fail(CSA2_ERR_INVALID_ARG, "rotary step is NULL or misaligned");
+  if (r->layout != CSA2_ROTARY_INTERLEAVED && r->layout != CSA2_ROTARY_HALF)
+    return fail(CSA2_ERR_INVALID_ARG, "bad rotary layout");
+  if (r->rot_dim < 2 || (r->rot_dim & 1)) return fail(CSA2_ERR_INVALID_ARG, "rot_dim must be even and at least 2");
+  if (r->first < 0 || r->rot_dim > dim || r->first > dim - r->rot_dim)
+    return fail(CSA2_ERR_SHAPE, "rotated dims outside the head");
+  if (!(r->scale - r->scale == 0.f)) return fail(CSA2_ERR_INVALID_ARG, "rotary scale must be finite");
+  return CSA2_OK;
+}
+
+csa2_status check_rotary_write(const csa2_rotary *kv, const csa2_rotary *ix, const void *kv_hat, const void *ix_hat) {
+  if (kv)
+    if (csa2_status s = check_rotary(kv, CSA2_MAIN_DIM)) return s;
+  if (ix)
+    if (csa2_status s = check_rotary(ix, CSA2_IX_DIM)) return s;
+  if (!aligned16(kv_hat) || !aligned8(ix_hat)) return fail(CSA2_ERR_INVALID_ARG, "kv_hat / ix_hat misaligned");
+  return CSA2_OK;
+}
+
+// Whether the heads of `out` lie apart from one another, tokens outermost or heads outermost.
+bool heads_apart(int64_t ts, int64_t hs, int64_t tokens, int64_t heads, int64_t dim) {
+  const bool by_token = (heads == 1 || hs >= dim) && (tokens == 1 || ts >= (heads - 1) * hs + dim);
+  const bool by_head = (tokens == 1 || ts >= dim) && (heads == 1 || hs >= (tokens - 1) * ts + dim);
+  return by_token || by_head;
+}
+
+}  // namespace
+
+CSA2_EXPORT csa2_status csa2_rotary_table(int32_t rot_dim, double base, csa2_rotary_scaling scaling, double factor,
+                                          int32_t original_len, double beta_fast, double beta_slow, uint64_t *step,
+                                          float *scale) {
+  if (!step) return fail(CSA2_ERR_INVALID_ARG, "step is NULL");
+  if (rot_dim < 2 || (rot_dim & 1)) return fail(CSA2_ERR_INVALID_ARG, "rot_dim must be even and at least 2");
+  if (scaling < CSA2_ROTARY_NONE || scaling > CSA2_ROTARY_YARN) return fail(CSA2_ERR_INVALID_ARG, "bad rotary scaling");
+  const double most = 1.7976931348623157e308;
+  if (!(base > 1.0 && base <= most) || !(factor >= 1.0 && factor <= most))
+    return fail(CSA2_ERR_INVALID_ARG, "need base > 1 and factor >= 1");
+  if (scaling == CSA2_ROTARY_NTK && rot_dim == 2) return fail(CSA2_ERR_INVALID_ARG, "NTK scaling needs rot_dim > 2");
+  if (scaling == CSA2_ROTARY_YARN && !(original_len > 0 && beta_slow > 0.0 && beta_fast > beta_slow && beta_fast <= most))
+    return fail(CSA2_ERR_INVALID_ARG, "YaRN needs original_len > 0 and beta_fast > beta_slow > 0");
+  csa2::rotary_table(rot_dim, base, scaling, factor, original_len, beta_fast, beta_slow, step, scale);
+  return CSA2_OK;
+}
+
+CSA2_EXPORT csa2_status csa2_rotate(const void *x, csa2_dtype x_dtype, int64_t x_token_stride, int64_t x_head_stride,
+                                    void *out, csa2_dtype out_dtype, int64_t out_token_stride, int64_t out_head_stride,
+                                    int32_t tokens, int32_t heads, int32_t dim, const int32_t *pos,
+                                    const csa2_rotary *rot, int32_t inverse, csa2_stream_t stream) {
+  if (tokens < 0 || heads < 0 || dim < 1) return fail(CSA2_ERR_INVALID_ARG, "bad size");
+  if (tokens == 0 || heads == 0) return CSA2_OK;
+  if (!x || !out || !pos || !rot) return fail(CSA2_ERR_INVALID_ARG, "NULL input");
+  if (!is_dtype(x_dtype) || !is_dtype(out_dtype)) return fail(CSA2_ERR_INVALID_ARG, "bad dtype");
+  if (csa2_status s = check_rotary(rot, dim)) return s;
+  if ((reinterpret_cast<uintptr_t>(x) & (x_dtype == CSA2_F32 ? 3 : 1)) ||
+      (reinterpret_cast<uintptr_t>(out) & (out_dtype == CSA2_F32 ? 3 : 1)))
+    return fail(CSA2_ERR_INVALID_ARG, "x / out misaligned");
+  if (x_token_stride < 0 || x_head_stride < 0 || out_token_stride < 0 || out_head_stride < 0)
+    return fail(CSA2_ERR_INVALID_ARG, "negative stride");
+  if (!heads_apart(out_token_stride, out_head_stride, tokens, heads, dim))
+    return fail(CSA2_ERR_SHAPE, "the heads of out overlap");
+  if (x == out && (x_dtype != out_dtype || x_token_stride != out_token_stride || x_head_stride != out_head_stride))
+    return fail(CSA2_ERR_INVALID_ARG, "in place needs the same type and strides");
+  csa2::launch_rotate(x, x_dtype, x_token_stride, x_head_stride, out, out_dtype, out_token_stride, out_head_stride,
+                      tokens, heads, dim, pos, *rot, inverse != 0, stream);
+  return launched("csa2_rotate");
+}
+
+CSA2_EXPORT csa2_status csa2_pack_kv_rotary(const void *lat_kv, const void *lat_ix, csa2_dtype dtype,
+                                            const float *pool_w, const float *gate_kv, const float *gate_ix, int32_t B,
+                                            int32_t T, const int32_t *first_entry, const csa2_rotary *rot_kv,
+                                            const csa2_rotary *rot_ix, const csa2_cache *cache, uint16_t *kv_hat,
+                                            uint16_t *ix_hat, int32_t *err, csa2_stream_t stream) {
+  if (B < 0 || T < 0) return fail(CSA2_ERR_INVALID_ARG, "negative size");
+  if (B == 0 || T == 0) return CSA2_OK;
+  if (csa2_status s = check_cache(cache, B)) return s;
+  if (!lat_kv || !lat_ix || !first_entry) return fail(CSA2_ERR_INVALID_ARG, "NULL input");
+  if (!is_dtype(dtype)) return fail(CSA2_ERR_INVALID_ARG, "bad dtype");
+  if ((gate_kv != nullptr) != (gate_ix != nullptr) || (gate_kv && pool_w))
+    return fail(CSA2_ERR_INVALID_ARG, "give gate_kv and gate_ix together, and no pool_w with them");
+  if (!aligned16(lat_kv) || (dtype == CSA2_F32 ? !aligned16(lat_ix) : !aligned8(lat_ix)) || !aligned16(gate_kv) ||
+      !aligned16(gate_ix))
+    return fail(CSA2_ERR_INVALID_ARG, "latents or gates misaligned");
+  if (csa2_status s = check_rotary_write(rot_kv, rot_ix, kv_hat, ix_hat)) return s;
+  if (int64_t(B) * (T / cache->ratio) > int64_t(INT32_MAX) * 8) return fail(CSA2_ERR_UNSUPPORTED, "too many entries per call");
+  csa2::launch_pack_kv_rotary(lat_kv, lat_ix, dtype, pool_w, gate_kv, gate_ix, B, T, first_entry, rot_kv, rot_ix,
+                              *cache, kv_hat, ix_hat, err, stream);
+  return launched("csa2_pack_kv_rotary");
+}
+
+CSA2_EXPORT csa2_status csa2_append_kv_rotary(const void *lat_kv, const void *lat_ix, csa2_dtype dtype, int32_t B,
+                                              const int32_t *pos, float *stage, const csa2_rotary *rot_kv,
+                                              const csa2_rotary *rot_ix, const csa2_cache *cache, uint16_t *kv_hat,
+                                              uint16_t *ix_hat, int32_t *err, csa2_stream_t stream) {
+  if (B < 0) return fail(CSA2_ERR_INVALID_ARG, "negative size");
+  if (B == 0) return CSA2_OK;
+  if (csa2_status s = check_cache(cache, B)) return s;
+  if (!lat_kv || !lat_ix || !pos) return fail(CSA2_ERR_INVALID_ARG, "NULL input");
+  if (!is_dtype(dtype)) return fail(CSA2_ERR_INVALID_ARG, "bad dtype");
+  if (!aligned16(lat_kv) || (dtype == CSA2_F32 ? !aligned16(lat_ix) : !aligned8(lat_ix)))
+    return fail(CSA2_ERR_INVALID_ARG, "latents misaligned");
+  if (cache->ratio > 1 && (!stage || !aligned16(stage)))
+    return fail(CSA2_ERR_INVALID_ARG, "ratio > 1 needs a 16-byte aligned staging buffer");
+  if (csa2_status s = check_rotary_write(rot_kv, rot_ix, kv_hat, ix_hat)) return s;
+  csa2::launch_append_kv_rotary(lat_kv, lat_ix, dtype, B, pos, stage,
+                                int64_t(cache->ratio) * (CSA2_MAIN_DIM + CSA2_IX_DIM), rot_kv, rot_ix, *cache,
+                                const_cast<int32_t *>(cache->num_entries), kv_hat, ix_hat, err, stream);
+  return launched("csa2_append_kv_rotary");
+}
+
+CSA2_EXPORT csa2_status csa2_pack_swa_rotary(const void *x, csa2_dtype dtype, int32_t B, int32_t T, const int32_t *pos,
+                                             const csa2_rotary *rot, uint8_t *swa_codes, float *swa_scale, int32_t R,
+                                             int32_t *err, csa2_stream_t stream) {
+  if (B < 0 || T < 0 || R < 1) return fail(CSA2_ERR_INVALID_ARG, "bad size");
+  if (B == 0 || T == 0) return CSA2_OK;
+  if (!x || !pos || !rot || !swa_codes || !swa_scale) return fail(CSA2_ERR_INVALID_ARG, "NULL input");
+  if (!is_dtype(dtype)) return fail(CSA2_ERR_INVALID_ARG, "bad dtype");
+  if (!aligned16(x) || !aligned16(swa_codes)) return fail(CSA2_ERR_INVALID_ARG, "x / swa_codes misaligned");
+  if (csa2_status s = check_rotary(rot, CSA2_SWA_DIM)) return s;
+  if (int64_t(B) * T > int64_t(INT32_MAX) * 8) return fail(CSA2_ERR_UNSUPPORTED, "too many tokens per call");
+  csa2::launch_pack_swa_rotary(x, dtype, B, T, pos, *rot, swa_codes, swa_scale, R, err, stream);
+  return launched("csa2_pack_swa_rotary");
+}
+
+// ---------------------------------------------------------------- attention over a shared prefix
+CSA2_EXPORT size_t csa2_prefix_workspace_size(int32_t B, int32_t Q, int32_t max_entries) {
+  if (B <= 0 || Q <= 0 || max_entries < 0) return 0;
+  const size_t rows = size_t(B) * Q;
+  return 2 * round256(rows * CSA2_HEADS * CSA2_MAIN_DIM * 4) + round256(rows * CSA2_HEADS * 4);
+}
+
+CSA2_EXPORT csa2_status csa2_prefix_attn(const uint16_t *q, int32_t B, int32_t Q, const int32_t *q_pos,
+                                         float softmax_scale, int32_t prefix_entries, int32_t max_entries,
+                                         const csa2_cache *cache, const uint8_t *swa_codes, const float *swa_scale,
+                                         int32_t R, int32_t window, void *o, csa2_dtype o_dtype, float *lse, void *ws,
+                                         size_t ws_bytes, int32_t *err, csa2_stream_t stream) {
+  if (B < 0 || Q < 0 || prefix_entries < 0 || max_entries < 0) return fail(CSA2_ERR_INVALID_ARG, "negative size");
+  if (B == 0 || Q == 0) return CSA2_OK;
+  if (csa2_status s = check_cache(cache, B)) return s;
+  if (!q || !q_pos || !o || !lse) return fail(CSA2_ERR_INVALID_ARG, "NULL input");
+  if (!is_dtype(o_dtype)) return fail(CSA2_ERR_INVALID_ARG, "bad dtype");
+  if (!aligned16(q) || !aligned16(o)) return fail(CSA2_ERR_INVALID_ARG, "q / o misaligned");
+  if (swa_codes) {
+    if (!swa_scale || window < 1 || window > 128 || R < window)
+      return fail(CSA2_ERR_INVALID_ARG, "need 1 <= window <= 128, window <= R");
+    if (!aligned16(swa_codes)) return fail(CSA2_ERR_INVALID_ARG, "swa_codes misaligned");
+  }
+  if (int64_t(B) * Q > 65535 * 16) return fail(CSA2_ERR_UNSUPPORTED, "too many query rows per call");
+  if (!ws || !aligned16(ws) || ws_bytes < csa2_prefix_workspace_size(B, Q, max_entries))
+    return fail(CSA2_ERR_INVALID_ARG, "workspace too small or misaligned");
+  const int64_t rows = int64_t(B) * Q;
+  const size_t part = round256(size_t(rows) * CSA2_HEADS * CSA2_MAIN_DIM * 4);
+  float *of = o_dtype == CSA2_F32 ? static_cast<float *>(o) : static_cast<float *>(ws);
+  float *po = reinterpret_cast<float *>(static_cast<char *>(ws) + part);
+  float *pl = reinterpret_cast<float *>(static_cast<char *>(ws) + 2 * part);
+  const int seg = csa2::attn_dense_segment();
+  for (int s = 0, e0 = 0; s == 0 || e0 < max_entries; ++s, e0 += seg) {
+    const int e1 = e0 + seg < max_entries ? e0 + seg : max_entries;
+    csa2::launch_attn_mma(q, B, Q, q_pos, softmax_scale, nullptr, 0, true, e0, e1, max_entries, cache,
+                          s == 0 ? swa_codes : nullptr, s == 0 && swa_codes ? swa_scale : nullptr, R, window,
+                          s == 0 ? of : po, s == 0 ? lse : pl, err, stream, nullptr, false, prefix_entries);
+    if (s > 0) csa2::launch_merge(of, lse, po, pl, rows * CSA2_HEADS, CSA2_MAIN_DIM, of, lse, stream);
+  }
+  if (o_dtype == CSA2_BF16)
+    csa2::launch_to_bf16(of, rows * CSA2_HEADS * CSA2_MAIN_DIM, static_cast<uint16_t *>(o), stream);
+  return launched("csa2_prefix_attn");
+}

@@ -89,6 +89,7 @@ struct AttnArgs {
   int k;
   int dense, e0, e1;
   int n_bound;  // dense: entries a query may see (more sets CSA2_ERR_SHAPE)
+  int prefix;   // dense: entries below it are sequence 0's
   csa2_cache c;
   // window source (codes == nullptr: none); with swa_new [rows][512] bf16, this step's token of
   // each row is quantised in the launch, used as the window's last key and stored in the ring
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1) attn_mma_kernel(AttnArgs p) {
           if (n < -1 || n >= nvis) {
             report(p.err, CSA2_ERR_INDEX);
           } else {
-            sl[r] = cache_slot(p.c, b, n);
+            sl[r] = cache_slot(p.c, n < p.prefix ? 0 : b, n);
             if (sl[r] < 0) report(p.err, CSA2_ERR_INDEX);
           }
         }
@@ -833,7 +834,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1) attn_tile_kernel(AttnArgs p) {
         if (n < -1 || n >= nvis) {
           if (half == 0) report(p.err, CSA2_ERR_INDEX);
         } else {
-          s = cache_slot(p.c, b, n);
+          s = cache_slot(p.c, n < p.prefix ? 0 : b, n);
           if (s < 0 && half == 0) report(p.err, CSA2_ERR_INDEX);
         }
       }
@@ -1093,13 +1094,13 @@ int attn_dense_segment() { return attn_clusters_fit<16>() > 0 ? 8192 : 4096; }
 void launch_attn_mma(const uint16_t *q, int B, int Q, const int32_t *q_pos, float tau, const int32_t *idx, int k,
                      bool dense, int e0, int e1, int n_bound, const csa2_cache *c, const uint8_t *codes,
                      const float *scale, int R, int window, float *o, float *lse, int32_t *err, cudaStream_t st,
-                     const uint16_t *swa_new, bool pdl) {
+                     const uint16_t *swa_new, bool pdl, int prefix) {
   const int rows = B * Q;
   if (rows == 0) return;
   AttnArgs a{};
   a.q = q, a.Q = Q, a.q_pos = q_pos, a.tau = tau;
   a.idx = dense ? nullptr : idx, a.k = (idx && !dense) ? k : 0;
-  a.dense = dense ? 1 : 0, a.e0 = e0, a.e1 = e1, a.n_bound = n_bound;
+  a.dense = dense ? 1 : 0, a.e0 = e0, a.e1 = e1, a.n_bound = n_bound, a.prefix = prefix;
   if (c) a.c = *c;
   a.codes = codes, a.scale = scale, a.R = R, a.window = window, a.swa_new = codes ? swa_new : nullptr;
   a.o = o, a.lse = lse, a.err = err;

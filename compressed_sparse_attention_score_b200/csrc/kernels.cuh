@@ -45,6 +45,22 @@ void launch_pack_swa(const void *x, csa2_dtype dtype, int B, int T, const int32_
 void launch_append_kv(const void *lat_kv, const void *lat_ix, csa2_dtype dtype, int B, const int32_t *pos,
                       float *stage, int64_t stage_stride, const csa2_cache &c, int32_t *num_entries, int32_t *err,
                       cudaStream_t st);
+// The rotating writers (rot_kv / rot_ix / hats may be NULL) and the rotation of heads.
+void launch_pack_kv_rotary(const void *lat_kv, const void *lat_ix, csa2_dtype dtype, const float *pool_w,
+                           const float *gate_kv, const float *gate_ix, int B, int T, const int32_t *first_entry,
+                           const csa2_rotary *rot_kv, const csa2_rotary *rot_ix, const csa2_cache &c, uint16_t *kv_hat,
+                           uint16_t *ix_hat, int32_t *err, cudaStream_t st);
+void launch_pack_swa_rotary(const void *x, csa2_dtype dtype, int B, int T, const int32_t *pos, const csa2_rotary &rot,
+                            uint8_t *codes, float *scale, int R, int32_t *err, cudaStream_t st);
+void launch_append_kv_rotary(const void *lat_kv, const void *lat_ix, csa2_dtype dtype, int B, const int32_t *pos,
+                             float *stage, int64_t stage_stride, const csa2_rotary *rot_kv, const csa2_rotary *rot_ix,
+                             const csa2_cache &c, int32_t *num_entries, uint16_t *kv_hat, uint16_t *ix_hat, int32_t *err,
+                             cudaStream_t st);
+void launch_rotate(const void *x, csa2_dtype xd, int64_t xt, int64_t xh, void *out, csa2_dtype od, int64_t ot,
+                   int64_t oh, int tokens, int heads, int dim, const int32_t *pos, const csa2_rotary &rot, bool inverse,
+                   cudaStream_t st);
+void rotary_table(int rot_dim, double base, csa2_rotary_scaling scaling, double factor, int original_len,
+                  double beta_fast, double beta_slow, uint64_t *step, float *scale);
 void launch_index_score_mma(const uint16_t *q_ix, const uint16_t *w, int B, int Q, const int32_t *q_pos,
                             const int32_t *cand, int P, int n_out, const csa2_cache &c, float *scores, int32_t *err,
                             cudaStream_t st);
@@ -71,7 +87,9 @@ void launch_topk_cluster(const float *scores, const int32_t *n_valid, int R, int
 void launch_attn_mma(const uint16_t *q, int B, int Q, const int32_t *q_pos, float tau, const int32_t *idx, int k,
                      bool dense, int e0, int e1, int n_bound, const csa2_cache *c, const uint8_t *codes,
                      const float *scale, int R, int window, float *o, float *lse, int32_t *err, cudaStream_t st,
-                     const uint16_t *swa_new = nullptr, bool pdl = false);
+                     const uint16_t *swa_new = nullptr, bool pdl = false, int prefix = 0);
+// n fp32 values (a multiple of 4) to bf16.
+void launch_to_bf16(const float *x, int64_t n, uint16_t *y, cudaStream_t st);
 // Entries per dense-attention launch (one cluster of at most 16 CTAs x 640 keys per row).
 int attn_dense_segment();
 void launch_merge(const float *o1, const float *l1, const float *o2, const float *l2, int64_t rows, int D_,

@@ -4,6 +4,7 @@
 // 16-byte vector loads, quantisation in registers, coalesced row stores.
 #include "common.cuh"
 #include "kernels.cuh"
+#include "rotary.cuh"
 
 namespace csa2 {
 
@@ -49,10 +50,23 @@ __device__ __forceinline__ void load4<uint16_t>(const uint16_t *p, float (&v)[4]
   v[2] = __uint_as_float(a.y << 16), v[3] = __uint_as_float(a.y & 0xFFFF0000u);
 }
 
+// Eight bf16 values of eight e2m1 codes (element 0 in the lowest nibble) times the scale s: at most
+// six significant bits, so exact in bf16.
+__device__ __forceinline__ uint4 hat8(uint32_t codes, float s) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = (__float_as_uint(e2m1_value((codes >> (8 * i)) & 15) * s) >> 16) |
+           (__float_as_uint(e2m1_value((codes >> (8 * i + 4)) & 15) * s) & 0xFFFF0000u);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Quantise the pooled entry a warp holds (lane l: main values [16l, 16l+16), one E4M3 block,
 // and indexer values [4l, 4l+4), eight lanes per E8M0 block) and store it at `slot`.
+// With kv_hat / ix_hat (rows of 512 and 128 bf16) the values that the codes stand for are stored too.
 __device__ __forceinline__ void store_entry(const float (&x)[16], const float (&xi)[4], int64_t slot,
-                                            const csa2_cache &c, int lane) {
+                                            const csa2_cache &c, int lane, uint16_t *kv_hat = nullptr,
+                                            uint16_t *ix_hat = nullptr) {
   // ---- main KV: E4M3 scale per 16 values, e2m1 codes
   float amax = 0.f;
 #pragma unroll
@@ -68,6 +82,10 @@ __device__ __forceinline__ void store_entry(const float (&x)[16], const float (&
   }
   reinterpret_cast<uint2 *>(c.kv_codes + slot * CSA2_MAIN_CODE_BYTES)[lane] = make_uint2(lo, hi);
   c.kv_scales[slot * CSA2_MAIN_SCALE_BYTES + lane] = uint8_t(sc);
+  if (kv_hat) {
+    reinterpret_cast<uint4 *>(kv_hat)[2 * lane] = hat8(lo, s);
+    reinterpret_cast<uint4 *>(kv_hat)[2 * lane + 1] = hat8(hi, s);
+  }
 
   // ---- indexer key: E8M0 exponent per 32 values (8 lanes), e2m1 codes
   float am = fmaxf(fmaxf(fabsf(xi[0]), fabsf(xi[1])), fmaxf(fabsf(xi[2]), fabsf(xi[3])));
@@ -83,6 +101,67 @@ __device__ __forceinline__ void store_entry(const float (&x)[16], const float (&
   }
   reinterpret_cast<uint16_t *>(c.ix_codes + slot * CSA2_IX_CODE_BYTES)[lane] = uint16_t(code4);
   if ((lane & 7) == 0) c.ix_scales[slot * CSA2_IX_SCALE_BYTES + (lane >> 3)] = uint8_t(ex + 127);
+  if (ix_hat) {
+    const uint4 v = hat8(code4, pow2f(ex));
+    reinterpret_cast<uint2 *>(ix_hat)[lane] = make_uint2(v.x, v.y);
+  }
+}
+
+// What the rotating writers add to the plain ones.
+struct RotaryWrite {
+  csa2_rotary kv, ix;  // rot_dim 0: not turned
+  bool same;           // both use one table and turn as many dims: one sine and cosine serve both
+  uint16_t *kv_hat, *ix_hat;
+};
+
+// Main value d of the row that a warp keeps in shared memory to turn it: four floats of padding
+// after every 16, so that the lanes' 16-value pieces start in different banks.
+__device__ __forceinline__ int turn_at(int d) { return d + 4 * (d >> 4); }
+constexpr int TURN_MAIN = D + 4 * (D / 16), TURN_ROW = TURN_MAIN + DI;
+
+// Pair (a, b) turned in fp64 and rounded once to fp32.
+__device__ __forceinline__ void turn_pair(float &a, float &b, double2 cs, float scale) {
+  const double x = a, y = b, g = scale;
+  a = float((x * cs.x - y * cs.y) * g);
+  b = float((x * cs.y + y * cs.x) * g);
+}
+
+// Turn the values a warp holds (x: main, lane l 16l ..; xi: indexer, lane l 4l .., or none) at
+// position pos: through the warp's row `buf` of shared memory, one pair per lane and step.
+template <bool IX>
+__device__ __forceinline__ void turn_values(float (&x)[16], float (&xi)[4], const csa2_rotary &kv, const csa2_rotary &ix,
+                                            bool same, int64_t pos, float *buf, int lane) {
+  __syncwarp();  // the row's previous use is over
+  if (kv.rot_dim) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4 *>(buf + turn_at(16 * lane) + 4 * i) =
+          make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+  }
+  if (IX && ix.rot_dim) *reinterpret_cast<float4 *>(buf + TURN_MAIN + 4 * lane) = make_float4(xi[0], xi[1], xi[2], xi[3]);
+  __syncwarp();
+  for (int i = lane; i < kv.rot_dim / 2; i += 32) {
+    const double2 cs = rotary_cs64(kv.step[i], pos);
+    turn_pair(buf[turn_at(rotary_dim0(kv, i))], buf[turn_at(rotary_dim1(kv, i))], cs, kv.scale);
+    if (IX && same)
+      turn_pair(buf[TURN_MAIN + rotary_dim0(ix, i)], buf[TURN_MAIN + rotary_dim1(ix, i)], cs, ix.scale);
+  }
+  if (IX && !same)
+    for (int i = lane; i < ix.rot_dim / 2; i += 32)
+      turn_pair(buf[TURN_MAIN + rotary_dim0(ix, i)], buf[TURN_MAIN + rotary_dim1(ix, i)],
+                rotary_cs64(ix.step[i], pos), ix.scale);
+  __syncwarp();
+  if (kv.rot_dim) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = *reinterpret_cast<const float4 *>(buf + turn_at(16 * lane) + 4 * i);
+      x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+    }
+  }
+  if (IX && ix.rot_dim) {
+    const float4 v = *reinterpret_cast<const float4 *>(buf + TURN_MAIN + 4 * lane);
+    xi[0] = v.x, xi[1] = v.y, xi[2] = v.z, xi[3] = v.w;
+  }
 }
 
 // exp(x) from a fixed sequence of fp32 operations (so that the gated compressor's weights,
@@ -109,20 +188,22 @@ __device__ __forceinline__ float exp_fixed(float x) {
 // (or fp32(1/r)), or with gate_kv / gate_ix the gated sum: per channel the softmax over the
 // entry's r tokens of the gate logits (max subtracted, exp_fixed, sum left to right, fp32
 // division) weights the tokens, summed left to right.
-template <typename T>
+// ROT: the entry is turned at its first token's position between pooling and quantisation.
+template <typename T, bool ROT>
 __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_kv,
                                                       const T *__restrict__ lat_ix,
                                                       const float *__restrict__ pool_w,
                                                       const float *__restrict__ gate_kv,
                                                       const float *__restrict__ gate_ix, int B, int T_,
                                                       const int32_t *__restrict__ first_entry,
-                                                      csa2_cache c, int32_t *err) {
+                                                      csa2_cache c, RotaryWrite rw, int32_t *err) {
   const int lane = threadIdx.x & 31;
+  __shared__ float turn_buf[ROT ? 8 : 1][ROT ? TURN_ROW : 1];
   const int n_new = T_ / c.ratio;
   const int64_t e = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (e >= int64_t(B) * n_new) return;
   const int b = int(e / n_new), j = int(e % n_new);
-  const int64_t slot = cache_slot(c, b, int64_t(first_entry[b]) + j);
+  const int64_t n = int64_t(first_entry[b]) + j, slot = cache_slot(c, b, n);
   if (slot < 0) {
     if (lane == 0) report(err, CSA2_ERR_INDEX);
     return;
@@ -130,6 +211,15 @@ __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_
   const float w_default = __fdiv_rn(1.0f, float(c.ratio));
   float x[16], xi[4];
   const int64_t tok0 = int64_t(b) * T_ + int64_t(j) * c.ratio;
+  auto finish = [&]() {
+    if constexpr (ROT) {
+      turn_values<true>(x, xi, rw.kv, rw.ix, rw.same, n * c.ratio, turn_buf[threadIdx.x >> 5], lane);
+      store_entry(x, xi, slot, c, lane, rw.kv_hat ? rw.kv_hat + e * D : nullptr,
+                  rw.ix_hat ? rw.ix_hat + e * DI : nullptr);
+    } else {
+      store_entry(x, xi, slot, c, lane);
+    }
+  };
 
   if (gate_kv) {
     // ---- gated sum: three passes over the group (max, normaliser, weighted sum)
@@ -175,7 +265,7 @@ __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_
         xi[i] = t == 0 ? term : __fadd_rn(xi[i], term);
       }
     }
-    store_entry(x, xi, slot, c, lane);
+    finish();
     return;
   }
 
@@ -192,7 +282,7 @@ __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_
     for (int i = 0; i < 4; ++i) xi[i] = t == 0 ? __fmul_rn(wt, vi[i]) : __fadd_rn(xi[i], __fmul_rn(wt, vi[i]));
   }
 
-  store_entry(x, xi, slot, c, lane);
+  finish();
 }
 
 // Decode-time append, one warp per sequence (lanes as in pack_kv_kernel).  The token at
@@ -201,12 +291,14 @@ __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_
 // right, weight fp32(1/r)) into entry pos / r, which is quantised and stored, and
 // num_entries[b] is raised to pos / r + 1.  Staging row t of sequence b (512 main then 128
 // indexer values) starts at stage + b * stage_stride + t * 640; stage may be NULL when r = 1.
-template <typename T>
+// ROT: a completed entry is turned at its first token's position before it is quantised.
+template <typename T, bool ROT>
 __global__ void __launch_bounds__(256) append_kv_kernel(const T *__restrict__ lat_kv, const T *__restrict__ lat_ix,
                                                         int B, const int32_t *__restrict__ pos, float *stage,
                                                         int64_t stage_stride, csa2_cache c, int32_t *num_entries,
-                                                        int32_t *err) {
+                                                        RotaryWrite rw, int32_t *err) {
   const int lane = threadIdx.x & 31;
+  __shared__ float turn_buf[ROT ? 8 : 1][ROT ? TURN_ROW : 1];
   const int b = int(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (b >= B) return;
   const int p = pos[b];
@@ -257,7 +349,13 @@ __global__ void __launch_bounds__(256) append_kv_kernel(const T *__restrict__ la
 #pragma unroll
     for (int i = 0; i < 4; ++i) xi[i] = t == 0 ? __fmul_rn(wt, ui[i]) : __fadd_rn(xi[i], __fmul_rn(wt, ui[i]));
   }
-  store_entry(x, xi, slot, c, lane);
+  if constexpr (ROT) {
+    turn_values<true>(x, xi, rw.kv, rw.ix, rw.same, int64_t(j) * r, turn_buf[threadIdx.x >> 5], lane);
+    store_entry(x, xi, slot, c, lane, rw.kv_hat ? rw.kv_hat + int64_t(b) * D : nullptr,
+                rw.ix_hat ? rw.ix_hat + int64_t(b) * DI : nullptr);
+  } else {
+    store_entry(x, xi, slot, c, lane);
+  }
   if (lane == 0 && num_entries) atomicMax(&num_entries[b], j + 1);
 }
 
@@ -265,13 +363,15 @@ __global__ void __launch_bounds__(256) append_kv_kernel(const T *__restrict__ la
 // tokens of a call are stored (earlier ones would be overwritten in the ring).  Ring b
 // takes its positions from row b % pos_rows of pos (several layers' rings of the same
 // sequences in one launch).
-template <typename T>
+// ROT: the token is turned at its own position first.
+template <typename T, bool ROT>
 __global__ void __launch_bounds__(256) pack_swa_kernel(const T *__restrict__ x, int B, int T_,
                                                        const int32_t *__restrict__ pos, int pos_rows,
                                                        uint8_t *__restrict__ codes,
-                                                       float *__restrict__ scale, int R,
+                                                       float *__restrict__ scale, int R, csa2_rotary rot,
                                                        int32_t *err) {
   const int lane = threadIdx.x & 31;
+  __shared__ float turn_buf[ROT ? 8 : 1][ROT ? TURN_MAIN : 1];
   const int64_t e = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (e >= int64_t(B) * T_) return;
   const int b = int(e / T_), t = int(e % T_);
@@ -281,6 +381,10 @@ __global__ void __launch_bounds__(256) pack_swa_kernel(const T *__restrict__ x, 
   const int64_t slot = int64_t(b) * R + (p % R);
   float v[16];
   load16<T>(x + e * D + 16 * lane, v);
+  if constexpr (ROT) {
+    float none[4];
+    turn_values<false>(v, none, rot, rot, false, p, turn_buf[threadIdx.x >> 5], lane);
+  }
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
@@ -296,43 +400,86 @@ __global__ void __launch_bounds__(256) pack_swa_kernel(const T *__restrict__ x, 
   if (lane == 0) scale[slot] = s;
 }
 
+// What the rotating writers are given, as the kernels take it.
+static RotaryWrite rotary_write(const csa2_rotary *kv, const csa2_rotary *ix, uint16_t *kv_hat, uint16_t *ix_hat) {
+  RotaryWrite w{};
+  if (kv) w.kv = *kv;
+  if (ix) w.ix = *ix;
+  w.same = kv && ix && kv->step == ix->step && kv->rot_dim == ix->rot_dim;
+  w.kv_hat = kv_hat, w.ix_hat = ix_hat;
+  return w;
+}
+
+template <typename T, bool ROT>
+static void pack_kv(const void *lat_kv, const void *lat_ix, const float *pool_w, const float *gate_kv,
+                    const float *gate_ix, int B, int T_, const int32_t *first_entry, const csa2_cache &c,
+                    const RotaryWrite &rw, int32_t *err, cudaStream_t st) {
+  const int64_t n = int64_t(B) * (T_ / c.ratio);
+  if (n == 0) return;
+  pack_kv_kernel<T, ROT><<<unsigned((n + 7) / 8), 256, 0, st>>>(static_cast<const T *>(lat_kv),
+                                                                static_cast<const T *>(lat_ix), pool_w, gate_kv,
+                                                                gate_ix, B, T_, first_entry, c, rw, err);
+}
+
 void launch_pack_kv(const void *lat_kv, const void *lat_ix, csa2_dtype dtype, const float *pool_w,
                     const float *gate_kv, const float *gate_ix, int B, int T, const int32_t *first_entry,
                     const csa2_cache &c, int32_t *err, cudaStream_t st) {
-  const int64_t n = int64_t(B) * (T / c.ratio);
+  const auto f = dtype == CSA2_F32 ? pack_kv<float, false> : pack_kv<uint16_t, false>;
+  f(lat_kv, lat_ix, pool_w, gate_kv, gate_ix, B, T, first_entry, c, RotaryWrite{}, err, st);
+}
+
+void launch_pack_kv_rotary(const void *lat_kv, const void *lat_ix, csa2_dtype dtype, const float *pool_w,
+                           const float *gate_kv, const float *gate_ix, int B, int T, const int32_t *first_entry,
+                           const csa2_rotary *rot_kv, const csa2_rotary *rot_ix, const csa2_cache &c, uint16_t *kv_hat,
+                           uint16_t *ix_hat, int32_t *err, cudaStream_t st) {
+  const auto f = dtype == CSA2_F32 ? pack_kv<float, true> : pack_kv<uint16_t, true>;
+  f(lat_kv, lat_ix, pool_w, gate_kv, gate_ix, B, T, first_entry, c, rotary_write(rot_kv, rot_ix, kv_hat, ix_hat), err,
+    st);
+}
+
+template <typename T, bool ROT>
+static void pack_swa(const void *x, int B, int T_, const int32_t *pos, int pos_rows, uint8_t *codes, float *scale,
+                     int R, const csa2_rotary &rot, int32_t *err, cudaStream_t st) {
+  const int64_t n = int64_t(B) * T_;
   if (n == 0) return;
-  const int grid = int((n + 7) / 8);
-  if (dtype == CSA2_F32)
-    pack_kv_kernel<float><<<grid, 256, 0, st>>>((const float *)lat_kv, (const float *)lat_ix, pool_w, gate_kv,
-                                                 gate_ix, B, T, first_entry, c, err);
-  else
-    pack_kv_kernel<uint16_t><<<grid, 256, 0, st>>>((const uint16_t *)lat_kv, (const uint16_t *)lat_ix, pool_w,
-                                                    gate_kv, gate_ix, B, T, first_entry, c, err);
+  pack_swa_kernel<T, ROT><<<unsigned((n + 7) / 8), 256, 0, st>>>(static_cast<const T *>(x), B, T_, pos, pos_rows, codes,
+                                                                 scale, R, rot, err);
 }
 
 void launch_pack_swa(const void *x, csa2_dtype dtype, int B, int T, const int32_t *pos, int pos_rows,
                      uint8_t *codes, float *scale, int R, int32_t *err, cudaStream_t st) {
-  const int64_t n = int64_t(B) * T;
-  if (n == 0) return;
-  const int grid = int((n + 7) / 8);
-  if (dtype == CSA2_F32)
-    pack_swa_kernel<float><<<grid, 256, 0, st>>>((const float *)x, B, T, pos, pos_rows, codes, scale, R, err);
-  else
-    pack_swa_kernel<uint16_t><<<grid, 256, 0, st>>>((const uint16_t *)x, B, T, pos, pos_rows, codes, scale, R,
-                                                    err);
+  const auto f = dtype == CSA2_F32 ? pack_swa<float, false> : pack_swa<uint16_t, false>;
+  f(x, B, T, pos, pos_rows, codes, scale, R, csa2_rotary{}, err, st);
+}
+
+void launch_pack_swa_rotary(const void *x, csa2_dtype dtype, int B, int T, const int32_t *pos, const csa2_rotary &rot,
+                            uint8_t *codes, float *scale, int R, int32_t *err, cudaStream_t st) {
+  const auto f = dtype == CSA2_F32 ? pack_swa<float, true> : pack_swa<uint16_t, true>;
+  f(x, B, T, pos, B, codes, scale, R, rot, err, st);
+}
+
+template <typename T, bool ROT>
+static void append_kv(const void *lat_kv, const void *lat_ix, int B, const int32_t *pos, float *stage,
+                      int64_t stage_stride, const csa2_cache &c, int32_t *num_entries, const RotaryWrite &rw,
+                      int32_t *err, cudaStream_t st) {
+  if (B == 0) return;
+  append_kv_kernel<T, ROT><<<(B + 7) / 8, 256, 0, st>>>(static_cast<const T *>(lat_kv), static_cast<const T *>(lat_ix),
+                                                        B, pos, stage, stage_stride, c, num_entries, rw, err);
 }
 
 void launch_append_kv(const void *lat_kv, const void *lat_ix, csa2_dtype dtype, int B, const int32_t *pos,
                       float *stage, int64_t stage_stride, const csa2_cache &c, int32_t *num_entries, int32_t *err,
                       cudaStream_t st) {
-  if (B == 0) return;
-  const int grid = (B + 7) / 8;
-  if (dtype == CSA2_F32)
-    append_kv_kernel<float><<<grid, 256, 0, st>>>((const float *)lat_kv, (const float *)lat_ix, B, pos, stage,
-                                                   stage_stride, c, num_entries, err);
-  else
-    append_kv_kernel<uint16_t><<<grid, 256, 0, st>>>((const uint16_t *)lat_kv, (const uint16_t *)lat_ix, B, pos,
-                                                      stage, stage_stride, c, num_entries, err);
+  const auto f = dtype == CSA2_F32 ? append_kv<float, false> : append_kv<uint16_t, false>;
+  f(lat_kv, lat_ix, B, pos, stage, stage_stride, c, num_entries, RotaryWrite{}, err, st);
+}
+
+void launch_append_kv_rotary(const void *lat_kv, const void *lat_ix, csa2_dtype dtype, int B, const int32_t *pos,
+                             float *stage, int64_t stage_stride, const csa2_rotary *rot_kv, const csa2_rotary *rot_ix,
+                             const csa2_cache &c, int32_t *num_entries, uint16_t *kv_hat, uint16_t *ix_hat, int32_t *err,
+                             cudaStream_t st) {
+  const auto f = dtype == CSA2_F32 ? append_kv<float, true> : append_kv<uint16_t, true>;
+  f(lat_kv, lat_ix, B, pos, stage, stage_stride, c, num_entries, rotary_write(rot_kv, rot_ix, kv_hat, ix_hat), err, st);
 }
 
 }  // namespace csa2

@@ -421,6 +421,120 @@ csa2_status csa2_sparse_attn_noalloc(csa2_mode mode, const uint16_t *q, int32_t 
                                      const float *swa_scale, int32_t R, int32_t window, float *o,
                                      float *lse, int32_t *err, csa2_stream_t stream);
 
+/*
+ * Rotary positions.  (The pages do not describe the position encoding; this is the published
+ * rotary form: each pair of dims is turned by an angle proportional to the token's position.)
+ * A rotation turns the rot_dim dims first .. first + rot_dim - 1 of a head and leaves the
+ * others.  Pair i of a head at position p:
+ *   (a, b) -> scale * (a cos t - b sin t, a sin t + b cos t),  t = 2 pi (p step[i] mod 2^64) / 2^64,
+ * where pair i is dims first + 2i, first + 2i + 1 (interleaved) or first + i, first + i +
+ * rot_dim / 2 (half).  step[i] counts 2^64ths of a turn per position, so the product of two
+ * integers, taken modulo 2^64, is the exact angle modulo one turn at every position (an fp32
+ * frequency is off by up to 2^-5 of a radian at position 2^20).
+ * The structure is host memory; step is a device pointer.
+ */
+typedef enum { CSA2_ROTARY_INTERLEAVED = 0, CSA2_ROTARY_HALF = 1 } csa2_rotary_layout;
+typedef struct {
+  const uint64_t *step; /* [rot_dim / 2] */
+  int32_t rot_dim;      /* dims turned: even, >= 2 */
+  int32_t first;        /* first of them */
+  int32_t layout;       /* a csa2_rotary_layout */
+  float scale;          /* multiplies the turned dims (1, or the table's attention scale) */
+} csa2_rotary;
+
+/*
+ * The steps of the usual frequencies base^(-2i / rot_dim), in extended precision, into step
+ * [rot_dim / 2] (HOST memory; the caller copies them to the device), and the scale that goes
+ * with them into *scale (optional).  Scaling for contexts `factor` times longer than original_len:
+ *   NONE    the frequencies as they are;
+ *   LINEAR  every frequency divided by factor (positions interpolated);
+ *   NTK     base * factor^(rot_dim / (rot_dim - 2)) in place of base (rot_dim > 2);
+ *   YARN    pairs that turn more than beta_fast times over original_len keep their frequency, those
+ *           that turn fewer than beta_slow times have it divided by factor, a linear ramp over the
+ *           pair index in between; scale = 0.1 ln(factor) + 1 (Peng et al., "YaRN", 2023).
+ * base > 1, factor >= 1; original_len, beta_fast > beta_slow > 0 are read for YARN only.
+ */
+typedef enum {
+  CSA2_ROTARY_NONE = 0,
+  CSA2_ROTARY_LINEAR = 1,
+  CSA2_ROTARY_NTK = 2,
+  CSA2_ROTARY_YARN = 3
+} csa2_rotary_scaling;
+csa2_status csa2_rotary_table(int32_t rot_dim, double base, csa2_rotary_scaling scaling, double factor,
+                              int32_t original_len, double beta_fast, double beta_slow, uint64_t *step,
+                              float *scale);
+
+/*
+ * Rotary positions applied to heads: query heads and indexer queries before they meet rotated
+ * keys, or (inverse) attention outputs, whose keys-as-values carry their positions.
+ *   x [tokens][heads][dim] in x_dtype, out the same shape in out_dtype (F32 or BF16 each), both
+ *   with unit stride along dim and the given strides (in elements) between tokens and heads;
+ *   pos [tokens] positions, a negative one marks a padding token, whose out is left as it is.
+ *   inverse != 0: the transposed rotation (sin negated) with the same scale, which is also the
+ *   gradient of the forward call with respect to x.
+ * Computed in fp32 and rounded once to out_dtype; dims that are not turned are copied.
+ * out == x (same type and strides) works in place and touches only the turned dims; otherwise out
+ * must not overlap x.  Any dim, head count and rotation; multiples of 8 with 16-byte aligned rows
+ * are fastest.
+ */
+csa2_status csa2_rotate(const void *x, csa2_dtype x_dtype, int64_t x_token_stride, int64_t x_head_stride,
+                        void *out, csa2_dtype out_dtype, int64_t out_token_stride, int64_t out_head_stride,
+                        int32_t tokens, int32_t heads, int32_t dim, const int32_t *pos,
+                        const csa2_rotary *rot, int32_t inverse, csa2_stream_t stream);
+
+/*
+ * csa2_pack_kv / csa2_pack_kv_gated with the rotation applied between pooling and quantisation:
+ * entry n of a cache of ratio r is turned at position n r, that of its group's first token.
+ *   rot_kv, rot_ix: rotations of the 512 main and the 128 indexer values (host structures; NULL:
+ *   those values are not turned).  The pooled fp32 values are turned in fp64 and rounded once to
+ *   fp32, so the codes do not depend on a math library; then quantised as csa2_pack_kv does.
+ *   pool_w as csa2_pack_kv, or gate_kv and gate_ix as csa2_pack_kv_gated (not both; all NULL: the mean).
+ *   kv_hat [B][T/r][512], ix_hat [B][T/r][128] bf16 (optional, NULL: none) receive the values that
+ *   the new entries' codes stand for, exactly (what attention will read back).
+ * Device errors: a slot outside the cache -> CSA2_ERR_INDEX in *err, entry and its hats skipped.
+ */
+csa2_status csa2_pack_kv_rotary(const void *lat_kv, const void *lat_ix, csa2_dtype dtype, const float *pool_w,
+                                const float *gate_kv, const float *gate_ix, int32_t B, int32_t T,
+                                const int32_t *first_entry, const csa2_rotary *rot_kv,
+                                const csa2_rotary *rot_ix, const csa2_cache *cache, uint16_t *kv_hat,
+                                uint16_t *ix_hat, int32_t *err, csa2_stream_t stream);
+
+/*
+ * csa2_append_kv with the rotation of csa2_pack_kv_rotary: a group that this token completes is
+ * pooled, turned at its first token's position and packed.  The staging rows stay unturned.
+ *   kv_hat [B][512], ix_hat [B][128] bf16 (optional): rows of sequences whose group was completed
+ *   receive the new entry's values, the others are left as they are.
+ */
+csa2_status csa2_append_kv_rotary(const void *lat_kv, const void *lat_ix, csa2_dtype dtype, int32_t B,
+                                  const int32_t *pos, float *stage, const csa2_rotary *rot_kv,
+                                  const csa2_rotary *rot_ix, const csa2_cache *cache, uint16_t *kv_hat,
+                                  uint16_t *ix_hat, int32_t *err, csa2_stream_t stream);
+
+/* csa2_pack_swa of tokens turned (as csa2_pack_kv_rotary turns entries) at their own positions. */
+csa2_status csa2_pack_swa_rotary(const void *x, csa2_dtype dtype, int32_t B, int32_t T, const int32_t *pos,
+                                 const csa2_rotary *rot, uint8_t *swa_codes, float *swa_scale, int32_t R,
+                                 int32_t *err, csa2_stream_t stream);
+
+/*
+ * Dense attention of a batch whose sequences share their first entries (one system prompt or
+ * document for many sessions; "DeepSeek V4.1 Flash 深度解析", 本专栏篇目 "前代 · HCA": dense
+ * attention over a heavily compressed cache).  As csa2_sparse_attn(CSA2_MODE_DENSE) with the
+ * optional window branch, except that entries n < prefix_entries of EVERY sequence are those of
+ * sequence 0: they are read through sequence 0's slots (and counted by each sequence's own
+ * num_entries), so one copy of the prefix serves the batch; entries n >= prefix_entries are the
+ * sequence's own.  prefix_entries = 0: no sharing.
+ *   q [B][Q][64][512] bf16; o [B][Q][64][512] in o_dtype (F32 or BF16); lse [B][Q][64] fp32.
+ *   max_entries bounds num_entries; visibility, window, empty rows and device errors as
+ *   csa2_sparse_attn.
+ * ws: csa2_prefix_workspace_size(B, Q, max_entries) bytes, 16-byte aligned, used by one call at a time.
+ */
+size_t csa2_prefix_workspace_size(int32_t B, int32_t Q, int32_t max_entries);
+csa2_status csa2_prefix_attn(const uint16_t *q, int32_t B, int32_t Q, const int32_t *q_pos,
+                             float softmax_scale, int32_t prefix_entries, int32_t max_entries,
+                             const csa2_cache *cache, const uint8_t *swa_codes, const float *swa_scale,
+                             int32_t R, int32_t window, void *o, csa2_dtype o_dtype, float *lse, void *ws,
+                             size_t ws_bytes, int32_t *err, csa2_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
