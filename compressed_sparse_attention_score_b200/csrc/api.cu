@@ -428,8 +428,7 @@ CSA2_EXPORT csa2_status csa2_pack_swa_rotary(const void *x, csa2_dtype dtype, in
 // ---------------------------------------------------------------- attention over a shared prefix
 CSA2_EXPORT size_t csa2_prefix_workspace_size(int32_t B, int32_t Q, int32_t max_entries) {
   if (B <= 0 || Q <= 0 || max_entries < 0) return 0;
-  const size_t rows = size_t(B) * Q;
-  return 2 * round256(rows * CSA2_HEADS * CSA2_MAIN_DIM * 4) + round256(rows * CSA2_HEADS * 4);
+  return csa2::prefix_workspace(int64_t(B) * Q, max_entries);
 }
 
 CSA2_EXPORT csa2_status csa2_prefix_attn(const uint16_t *q, int32_t B, int32_t Q, const int32_t *q_pos,
@@ -448,23 +447,13 @@ CSA2_EXPORT csa2_status csa2_prefix_attn(const uint16_t *q, int32_t B, int32_t Q
       return fail(CSA2_ERR_INVALID_ARG, "need 1 <= window <= 128, window <= R");
     if (!aligned16(swa_codes)) return fail(CSA2_ERR_INVALID_ARG, "swa_codes misaligned");
   }
-  if (int64_t(B) * Q > 65535 * 16) return fail(CSA2_ERR_UNSUPPORTED, "too many query rows per call");
+  if (!(softmax_scale - softmax_scale == 0.f)) return fail(CSA2_ERR_INVALID_ARG, "softmax_scale must be finite");
+  // (key tiles are counted in 32 bits)
+  if (int64_t(B) * Q > 65535 * 16 || int64_t(B) * Q * ((int64_t(max_entries) + 255) / 128) > INT32_MAX / 2)
+    return fail(CSA2_ERR_UNSUPPORTED, "too many query rows per call");
   if (!ws || !aligned16(ws) || ws_bytes < csa2_prefix_workspace_size(B, Q, max_entries))
     return fail(CSA2_ERR_INVALID_ARG, "workspace too small or misaligned");
-  const int64_t rows = int64_t(B) * Q;
-  const size_t part = round256(size_t(rows) * CSA2_HEADS * CSA2_MAIN_DIM * 4);
-  float *of = o_dtype == CSA2_F32 ? static_cast<float *>(o) : static_cast<float *>(ws);
-  float *po = reinterpret_cast<float *>(static_cast<char *>(ws) + part);
-  float *pl = reinterpret_cast<float *>(static_cast<char *>(ws) + 2 * part);
-  const int seg = csa2::attn_dense_segment();
-  for (int s = 0, e0 = 0; s == 0 || e0 < max_entries; ++s, e0 += seg) {
-    const int e1 = e0 + seg < max_entries ? e0 + seg : max_entries;
-    csa2::launch_attn_mma(q, B, Q, q_pos, softmax_scale, nullptr, 0, true, e0, e1, max_entries, cache,
-                          s == 0 ? swa_codes : nullptr, s == 0 && swa_codes ? swa_scale : nullptr, R, window,
-                          s == 0 ? of : po, s == 0 ? lse : pl, err, stream, nullptr, false, prefix_entries);
-    if (s > 0) csa2::launch_merge(of, lse, po, pl, rows * CSA2_HEADS, CSA2_MAIN_DIM, of, lse, stream);
-  }
-  if (o_dtype == CSA2_BF16)
-    csa2::launch_to_bf16(of, rows * CSA2_HEADS * CSA2_MAIN_DIM, static_cast<uint16_t *>(o), stream);
+  csa2::launch_prefix_attn(q, B, Q, q_pos, softmax_scale, prefix_entries, max_entries, *cache, swa_codes, swa_scale, R,
+                           window, o, o_dtype == CSA2_BF16, lse, ws, err, stream);
   return launched("csa2_prefix_attn");
 }

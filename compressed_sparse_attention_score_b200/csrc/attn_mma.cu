@@ -31,6 +31,7 @@
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
+#include "attn_common.cuh"
 #include "common.cuh"
 #include "kernels.cuh"
 #include "sm100.cuh"
@@ -89,7 +90,6 @@ struct AttnArgs {
   int k;
   int dense, e0, e1;
   int n_bound;  // dense: entries a query may see (more sets CSA2_ERR_SHAPE)
-  int prefix;   // dense: entries below it are sequence 0's
   csa2_cache c;
   // window source (codes == nullptr: none); with swa_new [rows][512] bf16, this step's token of
   // each row is quantised in the launch, used as the window's last key and stored in the ring
@@ -100,16 +100,6 @@ struct AttnArgs {
   float *o, *lse;
   int32_t *err;
 };
-
-// Offsets inside the swizzled operand layouts (bytes).
-// K-major, 128-byte rows, 1 KB atoms of 8 rows: 16-byte unit u of row r.
-__device__ __forceinline__ int kmaj128(int r, int u) { return (r >> 3) * 1024 + (r & 7) * 128 + ((u ^ (r & 7)) << 4); }
-// MN-major, 128-byte swizzle: element block (m / 64) at LBO 8192, K-row k: unit u of 8 M-elements.
-__device__ __forceinline__ int mnmaj128(int k, int mblk, int u) {
-  return mblk * 8192 + (k >> 3) * 1024 + (k & 7) * 128 + ((u ^ (k & 7)) << 4);
-}
-// MN-major, 64-byte swizzle (P^T): K-row k (key), unit u of 8 heads.
-__device__ __forceinline__ int mnmaj64(int k, int u) { return (k >> 3) * 512 + (k & 7) * 64 + ((u ^ ((k & 7) >> 1)) << 4); }
 
 // Query prescale.  The query heads enter the fp16 MMA multiplied by a power of two 2^s per
 // head that puts the head's largest |q| in [2^14, 2^15): every bf16 value within a factor
@@ -131,13 +121,6 @@ __device__ __forceinline__ void publish_query_max(const uint4 (&qraw)[qu_of<HG>(
     mb = __reduce_max_sync(0xffffffffu, mb);
     if ((threadIdx.x & 31) == 0) qmx[warp * QU + u] = mb;
   }
-}
-// Exponent s of the prescale of a head whose largest |bf16| bit pattern is mb (0 for an all-zero
-// or non-finite head).  floor(log2 max) = E - 127 for the biased exponent E.
-__device__ __forceinline__ int query_prescale_exp(uint32_t mb) {
-  const int E = int(mb >> 7);
-  if (mb == 0 || E >= 255) return 0;
-  return min(126, 141 - max(E, 1));
 }
 template <int HG = AM_HG>
 __device__ __forceinline__ uint32_t head_max_bits(const uint32_t *qmx, int h) {
@@ -265,26 +248,6 @@ __device__ __forceinline__ void quantise_new_token(const AttnArgs &p, uint2 u, i
     if (tid == 0) *new_scale = s;
   }
   __syncthreads();
-}
-
-// Max or sum over the 32 lanes of each of 32 per-lane values: afterwards lane l
-// holds the reduction of value index l.  31 shuffles (reduce-scatter butterfly).
-template <bool MAX>
-__device__ __forceinline__ float reduce_scatter32(float (&v)[32]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int width = 16; width >= 1; width >>= 1) {
-    const bool upper = lane & width;
-#pragma unroll
-    for (int i = 0; i < width; ++i) {
-      // keep the half selected by this lane's bit, send the other half
-      const float send = upper ? v[i] : v[i + width];
-      const float keep = upper ? v[i + width] : v[i];
-      const float got = __shfl_xor_sync(0xffffffffu, send, width);
-      v[i] = MAX ? fmaxf(keep, got) : keep + got;
-    }
-  }
-  return v[0];
 }
 
 // Cluster epilogue of a key-split row.  Partial of this CTA's keys: O_s (relative to its own
@@ -475,7 +438,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1) attn_mma_kernel(AttnArgs p) {
           if (n < -1 || n >= nvis) {
             report(p.err, CSA2_ERR_INDEX);
           } else {
-            sl[r] = cache_slot(p.c, n < p.prefix ? 0 : b, n);
+            sl[r] = cache_slot(p.c, b, n);
             if (sl[r] < 0) report(p.err, CSA2_ERR_INDEX);
           }
         }
@@ -834,7 +797,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1) attn_tile_kernel(AttnArgs p) {
         if (n < -1 || n >= nvis) {
           if (half == 0) report(p.err, CSA2_ERR_INDEX);
         } else {
-          s = cache_slot(p.c, n < p.prefix ? 0 : b, n);
+          s = cache_slot(p.c, b, n);
           if (s < 0 && half == 0) report(p.err, CSA2_ERR_INDEX);
         }
       }
@@ -1094,13 +1057,13 @@ int attn_dense_segment() { return attn_clusters_fit<16>() > 0 ? 8192 : 4096; }
 void launch_attn_mma(const uint16_t *q, int B, int Q, const int32_t *q_pos, float tau, const int32_t *idx, int k,
                      bool dense, int e0, int e1, int n_bound, const csa2_cache *c, const uint8_t *codes,
                      const float *scale, int R, int window, float *o, float *lse, int32_t *err, cudaStream_t st,
-                     const uint16_t *swa_new, bool pdl, int prefix) {
+                     const uint16_t *swa_new, bool pdl) {
   const int rows = B * Q;
   if (rows == 0) return;
   AttnArgs a{};
   a.q = q, a.Q = Q, a.q_pos = q_pos, a.tau = tau;
   a.idx = dense ? nullptr : idx, a.k = (idx && !dense) ? k : 0;
-  a.dense = dense ? 1 : 0, a.e0 = e0, a.e1 = e1, a.n_bound = n_bound, a.prefix = prefix;
+  a.dense = dense ? 1 : 0, a.e0 = e0, a.e1 = e1, a.n_bound = n_bound;
   if (c) a.c = *c;
   a.codes = codes, a.scale = scale, a.R = R, a.window = window, a.swa_new = codes ? swa_new : nullptr;
   a.o = o, a.lse = lse, a.err = err;

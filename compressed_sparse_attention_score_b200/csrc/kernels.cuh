@@ -87,9 +87,13 @@ void launch_topk_cluster(const float *scores, const int32_t *n_valid, int R, int
 void launch_attn_mma(const uint16_t *q, int B, int Q, const int32_t *q_pos, float tau, const int32_t *idx, int k,
                      bool dense, int e0, int e1, int n_bound, const csa2_cache *c, const uint8_t *codes,
                      const float *scale, int R, int window, float *o, float *lse, int32_t *err, cudaStream_t st,
-                     const uint16_t *swa_new = nullptr, bool pdl = false, int prefix = 0);
-// n fp32 values (a multiple of 4) to bf16.
-void launch_to_bf16(const float *x, int64_t n, uint16_t *y, cudaStream_t st);
+                     const uint16_t *swa_new = nullptr, bool pdl = false);
+// Dense attention whose first `prefix` entries are sequence 0's for every sequence, with the window
+// (codes may be NULL); ws holds prefix_workspace(B * Q, max_entries) bytes.
+size_t prefix_workspace(int64_t rows, int max_entries);
+void launch_prefix_attn(const uint16_t *q, int B, int Q, const int32_t *q_pos, float tau, int prefix, int max_entries,
+                        const csa2_cache &c, const uint8_t *codes, const float *scale, int R, int window, void *o,
+                        bool o_bf16, float *lse, void *ws, int32_t *err, cudaStream_t st);
 // Entries per dense-attention launch (one cluster of at most 16 CTAs x 640 keys per row).
 int attn_dense_segment();
 void launch_merge(const float *o1, const float *l1, const float *o2, const float *l2, int64_t rows, int D_,

@@ -34,18 +34,6 @@ __global__ void __launch_bounds__(256) merge_kernel(const float *o1, const float
   if (lane == 0) lse[r] = out_l;
 }
 
-__global__ void __launch_bounds__(256) to_bf16_kernel(const float *x, int64_t n, uint16_t *y) {
-  const int64_t i = 4 * (int64_t(blockIdx.x) * 256 + threadIdx.x);
-  if (i >= n) return;
-  const float4 v = *reinterpret_cast<const float4 *>(x + i);
-  *reinterpret_cast<__nv_bfloat162 *>(y + i) = __floats2bfloat162_rn(v.x, v.y);
-  *reinterpret_cast<__nv_bfloat162 *>(y + i + 2) = __floats2bfloat162_rn(v.z, v.w);
-}
-
-void launch_to_bf16(const float *x, int64_t n, uint16_t *y, cudaStream_t st) {
-  if (n) to_bf16_kernel<<<unsigned((n / 4 + 255) / 256), 256, 0, st>>>(x, n, y);
-}
-
 void launch_merge(const float *o1, const float *l1, const float *o2, const float *l2, int64_t rows, int D_,
                   float *o, float *lse, cudaStream_t st) {
   if (rows == 0) return;
