@@ -74,6 +74,8 @@ void launch_reindex_select(const uint16_t *q_ix, const uint16_t *w, int B, int Q
                            cudaStream_t st);
 // Tensor map of a cache's indexer codes as 128-entry groups (false: the layout does not allow one).
 bool make_index_code_map(CUtensorMap *m, const csa2_cache &c);
+// Tensor map of n rows of 512 fp16 values as 128 x 64 boxes (false: the encoder is missing).
+bool make_half_rows_map(CUtensorMap *m, const void *rows, int64_t n);
 // Fused prefill indexer + causal top-k (k <= 512): idx [B][Q][k], ascending, -1 padded.
 // Entries beyond max_entries are left out and set CSA2_ERR_SHAPE (as the unfused Full path).
 void launch_prefill_index(const uint16_t *q_ix, const uint16_t *w, int B, int Q, const int32_t *q_pos, int k,

@@ -2,22 +2,28 @@
 //
 // For a query token's 64 heads q_h and its keys v_j (512-d main entries, used as key and value, then
 // window tokens): x_hj = tau q_h . v_j, o_h = sum_j e^(x_hj - m_h) v_j / sum_j e^(x_hj - m_h), in one pass
-// over the keys with a running reference m_h.  Entries below `prefix` are read through sequence 0's slots
-// by every sequence, so the batch's blocks read one copy of them, from L2 after the first.
+// over the keys with a running reference m_h.
+//
+// Shared entries are dequantised once for the whole batch: expand_kernel writes them to the workspace in fp16
+// (e2m1 x E4M3 has at most six significant bits: exact; held as 2^-7 of the value), and every row's tiles of them
+// are TMA copies from L2.  Own entries, window tokens and the prefix's last, incomplete tile are dequantised
+// in the attention kernel, as is the whole prefix where too few rows share it.
 //
 // A persistent block per SM takes an equal share of the batch's 128-key tiles, in row order; a row whose
 // tiles lie in several blocks is left as partial (O, m, l) in the workspace and joined by combine_kernel.
 // Within a block, per tile:
-//   8 producer warps   dequantise the tile once (e2m1 x E4M3 to fp16: exact) into 128 KB of shared memory,
-//                      8 blocks of 64 dims, 128-byte swizzle: the K-major A operand of S^T = K Q^T and, the
-//                      same bytes, the MN-major A operand of O^T += V^T P^T;
-//   1 issuing thread   32 + 32 tcgen05.mma of 128 x 64 x 16 (M = keys or dims, N = the 64 heads); O^T stays in
+//   the key tile       128 KB of shared memory, 8 blocks of 64 dims, 128-byte swizzle: the K-major A operand of
+//                      S^T = K Q^T and, the same bytes, the MN-major A operand of O^T += V^T P^T; written by
+//   1 loading warp     (shared tiles, TMA) or by
+//   4 producer warps   (the others), a pair of blocks as soon as the previous tile's products have read it;
+//   1 issuing warp     32 + 32 tcgen05.mma of 128 x 64 x 16 (M = keys or dims, N = the 64 heads); O^T stays in
 //                      TMEM (4 x 64 columns) over all tiles of a row;
 //   8 softmax warps    read S^T (a lane is a key, a register a head), exponentiate and write P^T in fp16.
 // The reference m_h moves only when a logit exceeds it by 2^LAG, so O^T is rarely rescaled; weights are held
 // as 2^(x - m + BIAS), which keeps weights down to 2^-29 of the largest in fp16 while 2^(LAG + BIAS) stays far
 // below its maximum.  The sums are fp32 of the unrounded weights.
 #include <cuda_fp16.h>
+#include <string.h>
 
 #include "attn_common.cuh"
 #include "common.cuh"
@@ -29,12 +35,14 @@ using namespace sm100;
 
 namespace {
 constexpr int PX_TILE = 128;                 // keys per tile
-constexpr int PX_PROD = 256, PX_SOFT = 256;  // producer and softmax threads (warps 0-7, 8-15)
-constexpr int PX_THREADS = PX_PROD + PX_SOFT + 128;  // the issuer's warpgroup has one working thread
-// Registers per thread after launch (96 x 640): 256 x 96 + 256 x 120 + 128 x 48 = 61440.
-constexpr int PX_REG_PROD = 96, PX_REG_SOFT = 120, PX_REG_ISSUE = 48;
-static_assert(PX_PROD * PX_REG_PROD + PX_SOFT * PX_REG_SOFT + 128 * PX_REG_ISSUE <= 96 * PX_THREADS,
+constexpr int PX_PROD = 128, PX_SOFT = 256;  // producer and softmax threads (warps 0-3, 4-11)
+constexpr int PX_ISSUE_WARP = 12, PX_LOAD_WARP = 13;
+constexpr int PX_THREADS = PX_PROD + PX_SOFT + 128;  // (the last warpgroup has two working warps)
+// Registers per thread after launch (128 x 512): 128 x 128 + 256 x 152 + 128 x 72 = 64512.
+constexpr int PX_REG_SOFT = 152, PX_REG_ISSUE = 72;
+static_assert(PX_PROD * 128 + PX_SOFT * PX_REG_SOFT + 128 * PX_REG_ISSUE <= 128 * PX_THREADS,
               "the warpgroups' registers exceed the block's");
+constexpr int PX_MIN_ROWS = 4;               // rows from which a shared prefix is dequantised ahead
 constexpr int PX_MAX_CTAS = 160;             // workspace is sized for at most this many blocks
 constexpr float PX_LAG = 5.f, PX_BIAS = 5.f;
 constexpr uint64_t PX_WAIT_NS = 2000000000ull;
@@ -44,7 +52,7 @@ constexpr int PX_K = 0;                           // key tile: 8 x 16 KB
 constexpr int PX_Q = PX_K + 8 * 16384;            // query heads in fp16: 8 chunks of 64 dims x 64 heads
 constexpr int PX_P = PX_Q + 8 * 8192;             // P^T: 128 keys x 64 heads fp16
 constexpr int PX_MUL = PX_P + 16384;              // [2][128] logit and weight multipliers of the tile's keys
-constexpr int PX_HEAD = PX_MUL + 2 * 128 * 8;     // [2][64] 2^-s and, [64], the references
+constexpr int PX_HEAD = PX_MUL + 2 * 128 * 8;     // per head: [64] logit factors, references, negated references
 constexpr int PX_RED = PX_HEAD + 3 * 64 * 4;      // [8 warps][32]
 constexpr int PX_QMX = PX_RED + 8 * 32 * 4;       // [8 warps][16] query maxima
 constexpr int PX_SCAN = PX_QMX + 8 * 16 * 4;      // 40 ints
@@ -69,6 +77,9 @@ struct PrefixArgs {
   int o_bf16;
   float *lse;
   int32_t *plan;  // [0] tiles per block; from [16]: first tile of each row, and the number of tiles
+  int shared;     // tiles of the prefix that are dequantised ahead (0: none),
+  uint16_t *rows16;  // their entries in fp16, 512 each,
+  int32_t *bad;      // and per tile whether one of its entries is outside the cache
   float *parts;   // two slots of PX_SLOT floats per block
   int32_t *err;
 };
@@ -106,96 +117,201 @@ struct Work {
     }
   }
   __device__ __forceinline__ bool ends_piece() const { return left == 1 || tile + 1 == k.tiles; }
+  // every key of the tile is among the first `limit` entries
+  __device__ __forceinline__ bool within(int limit) const { return (tile + 1) * PX_TILE <= min(limit, k.nks); }
 };
 
-__device__ __forceinline__ int64_t entry_slot(const PrefixArgs &p, int b, int n) {
-  int64_t s;
-  if (p.c.page_table == nullptr) {
-    if (n >= p.c.seq_stride) return -1;
-    s = int64_t(b) * p.c.seq_stride + n;
-  } else {
-    const int page = n >> p.page_shift;
-    if (page >= p.c.max_pages) return -1;
-    const int32_t pid = p.c.page_table[int64_t(b) * p.c.max_pages + page];
-    if (pid < 0) return -1;
-    s = (int64_t(pid) << p.page_shift) + (n & (p.c.page_size - 1));
+// Slot of entry j of sequence b, given its page table's entry for it (-1: none); NO_SLOT if outside the cache.
+// (A slot's bytes are in memory, so its number fits 32 bits.)
+constexpr uint32_t NO_SLOT = 0xFFFFFFFFu;
+__device__ __forceinline__ int32_t entry_page(const PrefixArgs &p, int b, int j) {
+  const int n = j >> p.page_shift;
+  return p.c.page_table && n < p.c.max_pages ? p.c.page_table[int64_t(b) * p.c.max_pages + n] : -1;
+}
+__device__ __forceinline__ uint32_t entry_slot(const PrefixArgs &p, int b, int j, int32_t page) {
+  int64_t s = -1;
+  if (p.c.page_table) {
+    if (page >= 0) s = (int64_t(page) << p.page_shift) + (j & (p.c.page_size - 1));
+  } else if (j < p.c.seq_stride) {
+    s = int64_t(b) * p.c.seq_stride + j;
   }
-  return s < p.c.num_slots ? s : -1;
+  return s >= 0 && s < p.c.num_slots ? uint32_t(s) : NO_SLOT;
 }
 
-// One key half (dims 256 half .. + 255) as the producer holds it between its loads and the tile.
-struct KeyHalf {
-  uint4 raw[9];  // an entry's 128 code bytes and 16 scale bytes
-  const uint8_t *codes;  // a window token's 256 codes (NULL: an entry or nothing)
-  uint32_t shift;        // 2^k in both halves: the token's power of two
-  bool valid;
-  float mu, pv;
-};
+// Eight 4-bit codes times 2^-7 s (s128: 2^7 s in both halves) in fp16: o[e] holds elements e and e + 4, the order that a
+// word unpacks to pairwise (the query and the output use the same order of dims).  A code's three magnitude bits,
+// moved to bits 9 - 11 of an fp16 number, are 2^-14 of its value (subnormal for 0.5, as in e2m1).
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t s128, uint32_t *o) {
+  o[0] = hmul2_u32(((w << 12) & 0x80008000u) | ((w << 9) & 0x0E000E00u), s128);
+  o[1] = hmul2_u32(((w << 8) & 0x80008000u) | ((w << 5) & 0x0E000E00u), s128);
+  o[2] = hmul2_u32(((w << 4) & 0x80008000u) | ((w << 1) & 0x0E000E00u), s128);
+  o[3] = hmul2_u32((w & 0x80008000u) | ((w >> 3) & 0x0E000E00u), s128);
+}
+// 2^7 times an E4M3 scale, in both halves (at most 57344).
+__device__ __forceinline__ uint32_t scale128(uint32_t byte) { return hmul2_u32(cvt_e4m3x2_f16x2(byte * 0x101u), 0x58005800u); }
 
-__device__ __forceinline__ void load_key(const PrefixArgs &p, const Work &w, int key_in, int half, KeyHalf &r) {
-  const int j = w.tile * PX_TILE + key_in;
-  r.codes = nullptr;
-  r.valid = false;
-  r.mu = __int_as_float(0x7FFFFFFF);  // NaN: no key
-  r.pv = 0.f;
-  if (j < w.k.nks) {
-    const int64_t s = entry_slot(p, j < p.prefix ? 0 : w.k.b, j);
-    if (s < 0) {
-      if (half == 0) report(p.err, CSA2_ERR_INDEX);
-      return;
+// The prefix's complete tiles in fp16, one block each.  Memory bound: 288 bytes read and 1 KB written an entry.
+__global__ void __launch_bounds__(256) prefix_expand_kernel(const __grid_constant__ PrefixArgs p) {
+  grid_dep_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j0 = blockIdx.x * PX_TILE + 16 * warp;
+  const uint32_t mine = lane < 16 ? entry_slot(p, 0, j0 + lane, entry_page(p, 0, j0 + lane)) : 0u;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    uint2 codes[4];
+    uint32_t sc[4], slot[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      slot[i] = __shfl_sync(0xffffffffu, mine, 4 * g + i);
+      codes[i] = make_uint2(0u, 0u);
+      sc[i] = 0u;
+      if (slot[i] != NO_SLOT) {
+        codes[i] = reinterpret_cast<const uint2 *>(p.c.kv_codes + int64_t(slot[i]) * CSA2_MAIN_CODE_BYTES)[lane];
+        sc[i] = p.c.kv_scales[int64_t(slot[i]) * CSA2_MAIN_SCALE_BYTES + lane];
+      }
     }
-    r.valid = true;
-    r.mu = p.tau2;
-    r.pv = 1.f;
-    const uint4 *src = reinterpret_cast<const uint4 *>(p.c.kv_codes + s * CSA2_MAIN_CODE_BYTES + half * 128);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.raw[i] = src[i];
-    r.raw[8] = *reinterpret_cast<const uint4 *>(p.c.kv_scales + s * CSA2_MAIN_SCALE_BYTES + half * 16);
-  } else if (j < w.k.nk) {
-    const int64_t s = int64_t(w.k.b) * p.R + (w.k.lo + (j - w.k.nks)) % p.R;
-    const float sc = p.scale[s];
-    // the token's scale is 2^k f: 2^k goes into the fp16 value (exact for -15 <= k <= 7, codes being
-    // multiples of 2^-9 up to 448), f into the logit and the weight
-    const int k = max(-15, min(7, int((__float_as_uint(sc) >> 23) & 255) - 127));
-    const float f = sc * pow2f(-k);
-    r.valid = true;
-    r.mu = p.tau2 * f;
-    r.pv = f;
-    const __half2 h = __float2half2_rn(pow2f(k));
-    r.shift = *reinterpret_cast<const uint32_t *>(&h);
-    r.codes = p.codes + s * CSA2_SWA_DIM + half * 256;
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h[8];
+      const uint32_t s = scale128(sc[i]);
+      unpack8(codes[i].x, s, h);
+      unpack8(codes[i].y, s, h + 4);
+      uint4 *o = reinterpret_cast<uint4 *>(p.rows16 + int64_t(j0 + 4 * g + i) * D) + 2 * lane;
+      o[0] = make_uint4(h[0], h[1], h[2], h[3]);
+      o[1] = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+  }
+  const int any = __syncthreads_or(mine == NO_SLOT);
+  if (threadIdx.x == 0) p.bad[blockIdx.x] = any;
+}
+
+// A producer thread's part of a tile: 32 dims of each pair of blocks, of four keys 8 apart.  A warp's load of 16 bytes
+// a thread covers 64 bytes of each of eight keys, and its 16-byte stores fall into all banks.
+struct KeyPart {
+  uint32_t slot[4];  // cache slot of an entry, ring slot of a window token; NO_SLOT: no key
+  int entries;       // keys of the tile below this are entries
+  uint4 raw[4];      // entries' codes in one pair of blocks
+  uint32_t sc[4];    // and their two scales
+};
+struct KeyPlace {
+  int key0;   // the first of its keys
+  int piece;  // which 32 dims of the pair
+};
+
+// The slots of the tile's keys.
+__device__ __forceinline__ void find_keys(const PrefixArgs &p, const Work &w, const KeyPlace &at, KeyPart &r) {
+  r.entries = w.k.nks - w.tile * PX_TILE;
+  int32_t page[4];  // (the four table entries are fetched together)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = w.tile * PX_TILE + at.key0 + 8 * i;
+    page[i] = j < w.k.nks ? entry_page(p, j < p.prefix ? 0 : w.k.b, j) : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = w.tile * PX_TILE + at.key0 + 8 * i;
+    r.slot[i] = j < w.k.nks ? entry_slot(p, j < p.prefix ? 0 : w.k.b, j, page[i]) : NO_SLOT;
+    if (j >= w.k.nks && j < w.k.nk) r.slot[i] = uint32_t(w.k.b) * p.R + (w.k.lo + (j - w.k.nks)) % p.R;
+  }
+  if (at.piece == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (r.slot[i] == NO_SLOT && at.key0 + 8 * i < r.entries) report(p.err, CSA2_ERR_INDEX);
   }
 }
 
-// Block c (64 dims) of the half into row key_in of its tile block.
-__device__ __forceinline__ void store_block(const KeyHalf &r, int c, int key_in, uint8_t *dst) {
+// The entries' codes and scales of pair d.
+__device__ __forceinline__ void load_keys(const PrefixArgs &p, const KeyPlace &at, int d, KeyPart &r) {
 #pragma unroll
-  for (int q2 = 0; q2 < 2; ++q2) {
-    uint32_t h16[16];
-    if (r.codes) {
-      const uint4 a = reinterpret_cast<const uint4 *>(r.codes)[4 * c + 2 * q2];
-      const uint4 b = reinterpret_cast<const uint4 *>(r.codes)[4 * c + 2 * q2 + 1];
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  for (int i = 0; i < 4; ++i)
+    if (at.key0 + 8 * i < r.entries && r.slot[i] != NO_SLOT) {
+      r.raw[i] = *reinterpret_cast<const uint4 *>(p.c.kv_codes + int64_t(r.slot[i]) * CSA2_MAIN_CODE_BYTES + 64 * d + at.piece * 16);
+      r.sc[i] = *reinterpret_cast<const uint16_t *>(p.c.kv_scales + int64_t(r.slot[i]) * CSA2_MAIN_SCALE_BYTES + 8 * d + at.piece * 2);
+    }
+}
+
+// A window token's scale as 2^k f: 2^(k - 7) goes into the fp16 values, f into the logit and the weight.  Codes
+// are multiples of 2^-9 up to 448, so that is exact for -8 <= k <= 14; for smaller scales down to k = -16 it is
+// off by 2^-10 of the token's largest value at most, its E4M3 codes by 2^-5.
+__device__ __forceinline__ int window_exponent(float scale) {
+  return max(-16, min(14, int((__float_as_uint(scale) >> 23) & 255) - 127));
+}
+
+// The factors of the logits and weights of the tile's keys (NaN: no key).
+__device__ __forceinline__ void store_factors(const PrefixArgs &p, const KeyPlace &at, const KeyPart &r, float2 *mul) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        h16[i] = hmul2_u32(cvt_e4m3x2_f16x2((w[i >> 1] >> (16 * (i & 1))) & 0xFFFF), r.shift);
-    } else if (r.valid) {
-      const uint4 a = r.raw[2 * c + q2];
-      const uint32_t sc = ((&r.raw[8].x)[c] >> (16 * q2)) & 0xFFFF;
-      const uint32_t s0 = cvt_e4m3x2_f16x2((sc & 0xFF) * 0x101u), s1 = cvt_e4m3x2_f16x2((sc >> 8) * 0x101u);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  for (int i = 0; i < 4; ++i) {
+    const int key = at.key0 + 8 * i;
+    float f = __int_as_float(0x7FFFFFFF);
+    if (r.slot[i] != NO_SLOT) {
+      f = 1.f;
+      if (key >= r.entries) {
+        const float sc = p.scale[r.slot[i]];
+        f = sc * pow2f(-window_exponent(sc));
+      }
+    }
+    mul[key] = make_float2(f, r.slot[i] != NO_SLOT ? f : 0.f);
+  }
+}
+
+// Dims 128 d + 32 piece .. + 31 of keys I and I + 1 in fp16, times 2^-7, in the order of unpack8.
+template <int I>
+__device__ __forceinline__ void dequant_keys(const PrefixArgs &p, const KeyPlace &at, const KeyPart &r, int d, uint32_t (&h)[32]) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        h16[i] = hmul2_u32(cvt_e2m1x2_f16x2((w[i >> 2] >> (8 * (i & 3))) & 0xFF), i < 8 ? s0 : s1);
+  for (int i = I; i < I + 2; ++i) {
+    uint32_t *hk = h + 16 * (i - I);
+    if (r.slot[i] == NO_SLOT) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) hk[e] = 0u;
+    } else if (at.key0 + 8 * i < r.entries) {
+      const uint32_t s0 = scale128(r.sc[i] & 0xFFu), s1 = scale128(r.sc[i] >> 8);
+      unpack8(r.raw[i].x, s0, hk);
+      unpack8(r.raw[i].y, s0, hk + 4);
+      unpack8(r.raw[i].z, s1, hk + 8);
+      unpack8(r.raw[i].w, s1, hk + 12);
     } else {
+      const __half2 two = __float2half2_rn(pow2f(window_exponent(p.scale[r.slot[i]]) - 7));
+      const uint32_t s = *reinterpret_cast<const uint32_t *>(&two);
+      const uint4 *src =
+          reinterpret_cast<const uint4 *>(p.codes + int64_t(r.slot[i]) * CSA2_SWA_DIM + 128 * d + 32 * at.piece);
+      const uint4 a = src[0], b = src[1];
+      const uint32_t w8[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int i = 0; i < 16; ++i) h16[i] = 0u;
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          hk[4 * v + e] = hmul2_u32(cvt_e4m3x2_f16x2(__byte_perm(w8[2 * v], w8[2 * v + 1], e | ((4 + e) << 4)) & 0xFFFF), s);
     }
+  }
+}
+
+// Those values into the pair of blocks at dst.
+template <int I>
+__device__ __forceinline__ void store_keys(const uint32_t (&h)[32], const KeyPlace &at, uint8_t *dst) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int v = 0; v < 4; ++v)
-      *reinterpret_cast<uint4 *>(dst + kmaj128(key_in, 4 * q2 + v)) =
-          make_uint4(h16[4 * v], h16[4 * v + 1], h16[4 * v + 2], h16[4 * v + 3]);
-  }
+      *reinterpret_cast<uint4 *>(dst + (at.piece >> 1) * 16384 + kmaj128(at.key0 + 8 * (I + i), 4 * (at.piece & 1) + v)) =
+          make_uint4(h[16 * i + 4 * v], h[16 * i + 4 * v + 1], h[16 * i + 4 * v + 2], h[16 * i + 4 * v + 3]);
+}
+
+// Barrier over the producer threads; returns the OR of `pred` over them.
+__device__ __forceinline__ bool prod_any(bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(pred))
+      : "memory");
+  return r != 0;
+}
+
+// One block of 64 dims of the prefix's tile `tile` into shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap *map, int block, int tile, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(64 * block), "r"(tile * PX_TILE), "r"(smem_u32(bar))
+      : "memory");
 }
 
 // Barrier over the softmax threads; returns the OR of `pred` over them.
@@ -209,16 +325,70 @@ __device__ __forceinline__ bool soft_any(bool pred) {
   return r != 0;
 }
 
+// D (+)= A B^T with operands `da` and `db` 16-byte units behind the descriptors whose low words are a and b (the high
+// words are the same for all: 1 KB between 8-row groups, 128-byte swizzle), issued by the lane with `leader`.  The
+// whole warp runs it, so that the descriptors stay in uniform registers: in a branch of one lane a product took
+// 90 clocks to issue, twice its execution.
+constexpr uint32_t DESC_HIGH = (1024 >> 4) | (1u << 14) | (uint32_t(LAYOUT_SWIZZLE_128B) << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo_bytes) { return (saddr >> 4) | ((lbo_bytes >> 4) << 16); }
+__device__ __forceinline__ void mma_at(uint32_t leader, uint32_t d_tmem, uint32_t a, uint32_t da, uint32_t b, uint32_t db,
+                                       uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, l;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %6, 0;\n\t"
+      "@l tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a + da), "r"(b + db), "r"(idesc), "r"(uint32_t(accumulate)), "n"(DESC_HIGH), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit_to(uint32_t leader, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %1, 0;\n\t"
+      "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
 // This warpgroup's registers per thread (all of its warps call it).
 template <int N>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+
+// Four heads' logit factors and negated references (nref stands 2 H floats behind qmu).  Volatile: kept where they
+// are used, or all heads' would take the registers at once.
+__device__ __forceinline__ void lds_pair(float4 &q, float4 &r, uint32_t at) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%8];\n\tld.shared.v4.f32 {%4, %5, %6, %7}, [%8 + %9];"
+               : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w), "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
+               : "r"(at), "n"(2 * H * 4)
+               : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// a += x, b += y, and a *= x, b *= y (one packed operation, each result rounded to nearest).
+__device__ __forceinline__ void add2(float &a, float &b, float x, float y) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+
+__device__ __forceinline__ void mul2(float &a, float &b, float x, float y) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmul.rn.f32x2 p, p, q;\n\t"
+      "mov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
 }
 
 __device__ __forceinline__ void tc_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -234,60 +404,74 @@ __device__ __forceinline__ void tc_st_32x32b_x32(uint32_t taddr, const uint32_t 
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // The query heads of `row` in fp16, scaled per head by a power of two (query_prescale_exp), into the Q
-// operand; qinv[h] = 2^-s.  Called by the softmax threads (t of 256); contains two barriers of theirs.
-__device__ __forceinline__ void load_query(const PrefixArgs &p, int row, uint8_t *smem, float *qinv, int t) {
+// operand; qmu[h] = 2^7 tau log2(e) 2^-s (the tile holds 2^-7 of the keys).  Called by the softmax threads (t of 256); contains two barriers of
+// theirs, the first before anything is written.
+__device__ __forceinline__ void load_query(const PrefixArgs &p, int row, uint8_t *smem, float *qmu, int t) {
   uint32_t *qmx = reinterpret_cast<uint32_t *>(smem + PX_QMX);
   const uint4 *src = reinterpret_cast<const uint4 *>(p.q + int64_t(row) * H * D);
-  uint4 v[16];
+  const int warp = t >> 5, pair = warp & ~1;  // the two warps that hold the heads t / 64 + 4 u
+  uint4 v[8];  // chunk t + 256 u: head t / 64 + 4 u, dims 8 (t % 64) ..; u = 8 half ..
+  auto load = [&](int half) {
 #pragma unroll
-  for (int u = 0; u < 16; ++u) v[u] = src[t + 256 * u];  // head t / 64 + 4 u, dims 8 (t % 64) ..
-  const int warp = t >> 5;
+    for (int u = 0; u < 8; ++u) v[u] = src[t + 256 * (8 * half + u)];
+  };
 #pragma unroll
-  for (int u = 0; u < 16; ++u) {
-    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-    uint32_t mb = 0;
+  for (int half = 1; half >= 0; --half) {
+    load(half);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mb = max(mb, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-    mb = __reduce_max_sync(0xffffffffu, mb);
-    if ((t & 31) == 0) qmx[warp * 16 + u] = mb;
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      uint32_t mb = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mb = max(mb, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+      mb = __reduce_max_sync(0xffffffffu, mb);
+      if ((t & 31) == 0) qmx[warp * 16 + 8 * half + u] = mb;
+    }
   }
   soft_any(false);
-  const int pair = warp & ~1;  // the two warps that hold the heads t / 64 + 4 u
 #pragma unroll
-  for (int u = 0; u < 16; ++u) {
-    const float sc = pow2f(query_prescale_exp(max(qmx[pair * 16 + u], qmx[pair * 16 + 16 + u])));
-    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-    uint32_t o4[4];
+  for (int half = 0; half < 2; ++half) {
+    if (half) load(half);  // (read twice: 16 chunks do not fit the registers beside the sums)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 hv = __floats2half2_rn(__uint_as_float(w[i] << 16) * sc, __uint_as_float(w[i] & 0xFFFF0000u) * sc);
-      o4[i] = *reinterpret_cast<const uint32_t *>(&hv);
+    for (int u = 0; u < 8; ++u) {
+      const int c = 8 * half + u;
+      const float sc = pow2f(query_prescale_exp(max(qmx[pair * 16 + c], qmx[pair * 16 + 16 + c])));
+      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      uint32_t o4[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // dims i and i + 4 of the eight
+        const uint32_t lo = w[i >> 1], hi = w[2 + (i >> 1)];
+        const __half2 hv = __floats2half2_rn(__uint_as_float((i & 1) ? lo & 0xFFFF0000u : lo << 16) * sc,
+                                             __uint_as_float((i & 1) ? hi & 0xFFFF0000u : hi << 16) * sc);
+        o4[i] = *reinterpret_cast<const uint32_t *>(&hv);
+      }
+      const int h = (t >> 6) + 4 * c, u8 = t & 63;
+      *reinterpret_cast<uint4 *>(smem + PX_Q + (u8 / 8) * 8192 + kmaj128(h, u8 % 8)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
     }
-    const int h = (t >> 6) + 4 * u, u8 = t & 63;
-    *reinterpret_cast<uint4 *>(smem + PX_Q + (u8 / 8) * 8192 + kmaj128(h, u8 % 8)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
   }
   if (t < H) {
     const int c = t & 3, u = t >> 2;
-    qinv[t] = pow2f(-query_prescale_exp(max(qmx[2 * c * 16 + u], qmx[(2 * c + 1) * 16 + u])));
+    qmu[t] = 128.f * p.tau2 * pow2f(-query_prescale_exp(max(qmx[2 * c * 16 + u], qmx[(2 * c + 1) * 16 + u])));
   }
   fence_proxy_async_smem();
   soft_any(false);
 }
 
-__global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid_constant__ PrefixArgs p) {
+__global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid_constant__ CUtensorMap map,
+                                                                     const __grid_constant__ PrefixArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float2 *mul = reinterpret_cast<float2 *>(smem + PX_MUL);
-  float *qinv = reinterpret_cast<float *>(smem + PX_HEAD);  // [2][64]
-  float *mref = qinv + 2 * H;
+  float *qmu = reinterpret_cast<float *>(smem + PX_HEAD);  // logit factor of each head
+  float *mref = qmu + H, *nref = mref + H;                 // reference m, and BIAS - m
   float *red = reinterpret_cast<float *>(smem + PX_RED);
   int *scan = reinterpret_cast<int *>(smem + PX_SCAN);
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + PX_BAR);  // [4] pair of blocks written (4 warps)
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + PX_BAR);  // [4] pair of blocks written
   uint64_t *freed = full + 4;                                    // [4] pair of blocks consumed
-  uint64_t *s_full = freed + 4, *p_full = s_full + 1, *q_full = s_full + 2, *o_full = s_full + 3, *idle = s_full + 4;
+  uint64_t *s_full = freed + 4, *o_full = s_full + 1, *p_full = s_full + 2, *q_full = s_full + 3, *idle = s_full + 4;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 5);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(s_full + 6);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   // ---- the plan: all rows' tiles, the tiles per block, and where this block's begin
   int sum = 0;
@@ -320,19 +504,26 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   }
   grid_dep_launch();
   if (t0 >= t1) return;
-  if (warp == 16) {
+  // entries below `limit` are read from the workspace: the shared tiles before the first bad one
+  int *limit_at = scan + 38;
+  if (tid == 0) *limit_at = p.shared;
+  grid_dep_wait();
+  __syncthreads();
+  for (int i = tid; i < p.shared; i += PX_THREADS)
+    if (p.bad[i]) atomicMin(limit_at, i);
+  if (warp == 0) {
     tmem_alloc(tmem_slot, PX_TMEM_COLS);
     tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&full[i], 4);
+      mbar_init(&full[i], 1);
       mbar_init(&freed[i], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(p_full, 8);
-    mbar_init(q_full, 8);
     mbar_init(o_full, 1);
+    mbar_init(p_full, 1);
+    mbar_init(q_full, 1);
     mbar_init(idle, 1);
     *abort_flag = 0;
     mbar_init_fence();
@@ -344,91 +535,238 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   Work w;
   w.row = first[0], w.tile = first[1], w.left = t1 - t0;
   w.k = row_keys(p, w.row);
+  const int limit = *limit_at * PX_TILE;
 
-  if (warp < 8) {
-    // ------------------------------------------------------------ producers: key tid % 128, half tid / 128
-    regs_down<PX_REG_PROD>();
-    const int key_in = tid & 127, half = tid >> 7;
-    KeyHalf r;
-    load_key(p, w, key_in, half, r);
-    for (int n = 0; w.left > 0; ++n) {
-      bool ok = true;
-#pragma unroll
-      for (int c2 = 0; c2 < 2; ++c2) {
-        const int d = 2 * half + c2;
-        if (n > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&freed[d], (n - 1) & 1, abort_flag, PX_WAIT_NS));
-        if (!ok) break;
-        if (c2 == 0 && half == 0) mul[(n & 1) * 128 + key_in] = make_float2(r.mu, r.pv);
-        store_block(r, 2 * c2, key_in, smem + PX_K + (2 * d) * 16384);
-        store_block(r, 2 * c2 + 1, key_in, smem + PX_K + (2 * d + 1) * 16384);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[d]);
+  if (warp < 4) {
+    // ------------------------------------------------------------ producers: warp w keys 32 w .. + 31
+    // Half of each piece is dequantised into registers before its blocks are free, so that little lies between
+    // the last product that reads a block and the first that reads its successor.
+    const KeyPlace at{32 * warp + (lane & 3) + 4 * ((lane >> 3) & 1), ((lane >> 2) & 1) + 2 * (lane >> 4)};
+    KeyPart r;
+    uint32_t h[32];
+    bool ok = true;
+    for (int n = 0; w.left > 0 && ok; ++n, w.next(p)) {
+      if (w.within(limit)) {  // not theirs; but a barrier's parity tells only its last two phases apart
+        ok = n == 0 || mbar_wait_bounded(&freed[3], (n - 1) & 1, abort_flag, PX_WAIT_NS);
+        ok = !prod_any(!ok);
+        continue;
       }
-      if (!ok) break;
-      w.next(p);
-      if (w.left > 0) load_key(p, w, key_in, half, r);
+      find_keys(p, w, at, r);
+      load_keys(p, at, 0, r);
+#pragma unroll 1
+      for (int d = 0; d < 4; ++d) {
+        uint8_t *dst = smem + PX_K + d * 2 * 16384;
+        dequant_keys<0>(p, at, r, d, h);
+        ok = n == 0 || mbar_wait_bounded(&freed[d], (n - 1) & 1, abort_flag, PX_WAIT_NS);
+        if (prod_any(!ok)) {
+          ok = false;
+          break;
+        }
+        if (d == 0 && at.piece == 0) store_factors(p, at, r, mul + (n & 1) * 128);
+        store_keys<0>(h, at, dst);
+        dequant_keys<2>(p, at, r, d, h);
+        if (d < 3) load_keys(p, at, d + 1, r);
+        store_keys<2>(h, at, dst);
+        fence_proxy_async_smem();
+        prod_any(false);
+        if (tid == 0) mbar_arrive(&full[d]);
+      }
     }
-  } else if (warp < 16) {
+  } else if (warp >= PX_ISSUE_WARP) {
+    regs_down<PX_REG_ISSUE>();
+    if (warp == PX_LOAD_WARP) {
+      // ---------------------------------------------------------- the loader of shared tiles
+      const uint32_t leader = elect_one(), kt = smem_u32(smem + PX_K);
+      if (p.shared > 0) asm volatile("fence.proxy.async;" ::: "memory");  // (the expansion's stores were generic ones)
+      bool ok = true;
+      int last[4] = {-1, -1, -1, -1}, never = 0;
+      for (int n = 0; w.left > 0 && ok; ++n, w.next(p)) {
+        if (!w.within(limit)) {  // (as above)
+          if (n > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&freed[3], (n - 1) & 1, abort_flag, PX_WAIT_NS));
+          continue;
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&freed[d], (n - 1) & 1, abort_flag, PX_WAIT_NS));
+          if (ok) last[d] = n;
+          if (ok && leader) {
+            mbar_arrive_expect_tx(&full[d], 2 * 16384);
+            tma_block(kt + (2 * d) * 16384, &map, 2 * d, w.tile, &full[d]);
+            tma_block(kt + (2 * d + 1) * 16384, &map, 2 * d + 1, w.tile, &full[d]);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok)  // given up: the copies under way still have to land before the block ends
+        for (int d = 0; d < 4; ++d)
+          if (last[d] >= 0) mbar_wait_bounded(&full[d], last[d] & 1, &never, PX_WAIT_NS);
+    }
+    // ------------------------------------------------------------ the tensor core's issuer
+    // O^T += V^T P^T for the 128 dims of a pair of blocks, and S^T of the next tile over them as soon as they are
+    // written, some steps behind their last use.
+    if (warp == PX_ISSUE_WARP) {
+      const uint32_t kt = smem_u32(smem + PX_K), qt = smem_u32(smem + PX_Q), pt = smem_u32(smem + PX_P);
+      const uint32_t leader = elect_one();
+      constexpr uint32_t id_s = idesc_f16(PX_TILE, H, false, false), id_o = idesc_f16(PX_TILE, H, true, true);
+      auto wait = [&](uint64_t *bar, int phase) {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, phase & 1, abort_flag, PX_WAIT_NS));
+        tc_fence_after();
+        return ok;
+      };
+      auto step_s = [&](int n, int d, bool opens) {
+        if (!wait(&full[d], n)) return false;
+        const uint32_t a = desc_low(kt, 16) + 2048 * d, b = desc_low(qt, 16) + 1024 * d;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4)
+            mma_at(leader, tmem + PX_TMEM_S, a, 1024 * c + 2 * k4, b, 512 * c + 2 * k4, id_s, !opens || c > 0 || k4 > 0);
+        return true;
+      };
+      auto step_o = [&](int d, bool opens) {
+        const uint32_t a = desc_low(kt, 16384) + 2048 * d, b = desc_low(pt, 16);
+#pragma unroll
+        for (int jc = 0; jc < 2; ++jc)
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4)
+            mma_at(leader, tmem + d * 64, a, 512 * jc + 128 * k4, b, 512 * jc + 128 * k4, id_o, !opens || jc > 0 || k4 > 0);
+        commit_to(leader, &freed[d]);
+      };
+      bool begins = true, more = true;
+      for (int n = 0, piece = 0; more; ++n) {
+        if (begins) {  // S^T of a piece's first tile
+          if (!wait(q_full, piece)) break;
+          if (!step_s(n, 0, true) || !step_s(n, 1, false) || !step_s(n, 2, false) || !step_s(n, 3, false)) break;
+          commit_to(leader, s_full);
+        }
+        const bool ends = w.ends_piece();
+        if (!wait(p_full, n)) break;
+        step_o(0, begins);
+        step_o(1, begins);
+        step_o(2, begins);
+        if (!ends && !step_s(n + 1, 0, true)) break;
+        step_o(3, begins);
+        if (ends) {
+          commit_to(leader, o_full);
+          ++piece;
+        } else {
+          if (!step_s(n + 1, 1, false) || !step_s(n + 1, 2, false) || !step_s(n + 1, 3, false)) break;
+          commit_to(leader, s_full);
+        }
+        w.next(p);
+        more = w.left > 0;
+        begins = ends;
+      }
+      if (more) {  // given up: the products under way still have to end before the block does
+        int never = 0;
+        commit_to(leader, idle);
+        mbar_wait_bounded(idle, 0, &never, PX_WAIT_NS);
+      }
+    }
+  } else {
     // ------------------------------------------------------------ softmax
     regs_up<PX_REG_SOFT>();
-    const int t = tid - PX_PROD, q4 = warp & 3, hb = 32 * ((warp - 8) >> 2), key = 32 * q4 + lane;
-    const uint32_t lanes = tmem + (uint32_t(32 * q4) << 16);
+    const int t = tid - PX_PROD, q4 = warp & 3, hb = 32 * ((warp - 4) >> 2), key = 32 * q4 + lane;
+    const uint32_t lanes = tmem + (uint32_t(32 * q4) << 16), head = smem_u32(qmu + hb);
     float sum_h[32];
     int piece = 0;
     bool begins = true, alive = true;
-    load_query(p, w.row, smem, qinv, t);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(q_full);
+    load_query(p, w.row, smem, qmu, t);
+    if (t == 0) mbar_arrive(q_full);
     for (int n = 0; w.left > 0; ++n) {
       const bool ok = mbar_wait_bounded(s_full, n & 1, abort_flag, PX_WAIT_NS);
       tc_fence_after();
-      uint32_t s[32];
       __syncwarp();
-      const float2 m2 = mul[(n & 1) * 128 + key];
+      const bool shared = w.within(limit);
+      const float2 m2 = shared ? make_float2(1.f, 1.f) : mul[(n & 1) * 128 + key];
       const bool valid = m2.x == m2.x;
-      const float4 *qi4 = reinterpret_cast<const float4 *>(qinv + (piece & 1) * H + hb);
-      float *mr = mref + hb;
-      // the logits in units of log 2 into s; returns how far they exceed the references
-      auto logits = [&]() {
-        tc_ld_32x32b_x32(lanes + PX_TMEM_S + hb, s);
-        tc_wait_ld();
-        float over = -INFINITY;
+      const bool plain = shared || __all_sync(0xffffffffu, m2.x == 1.f);  // this warp's keys are all entries
+      float s[32];
+      // The weights 2^(logit - reference + BIAS) into s and, times the keys' factors, in fp16 into P^T;
+      // returns the largest exponent.
+      auto weights = [&]() {
+        float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 qi = qi4[i], m4 = reinterpret_cast<const float4 *>(mr)[i];
-          const float qs[4] = {qi.x, qi.y, qi.z, qi.w}, ms[4] = {m4.x, m4.y, m4.z, m4.w};
+        for (int g = 0; g < 2; ++g) {  // 16 heads at a time
+          tc_ld_32x32b_x16(lanes + PX_TMEM_S + hb + 16 * g, reinterpret_cast<uint32_t(&)[16]>(s[16 * g]));
+          tc_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = valid ? (m2.x * __uint_as_float(s[4 * i + e])) * qs[e] : -INFINITY;
-            s[4 * i + e] = __float_as_uint(x);
-            over = fmaxf(over, x - ms[e]);
+          for (int i = 4 * g; i < 4 * g + 4; ++i) {
+            float4 q, r;
+            lds_pair(q, r, head + 16 * i);
+            float x[4] = {s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]};
+            if (!plain) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] *= m2.x;
+            }
+            // (product and difference rounded one after the other, as the references are formed: a fused one would
+            // differ from them by more than the lag where logits are very large)
+            mul2(x[0], x[1], q.x, q.y);
+            mul2(x[2], x[3], q.z, q.w);
+            add2(x[0], x[1], r.x, r.y);
+            add2(x[2], x[3], r.z, r.w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (!plain) x[e] = valid ? x[e] : -INFINITY;
+              top = fmaxf(top, x[e]);
+              s[4 * i + e] = ex2(x[e]);
+            }
           }
+          uint32_t ph[8];
+#pragma unroll
+          for (int h = 0; h < 16; h += 2) {
+            const float e0 = s[16 * g + h], e1 = s[16 * g + h + 1];
+            const __half2 hp = plain ? __floats2half2_rn(e0, e1) : __floats2half2_rn(e0 * m2.y, e1 * m2.y);
+            ph[h >> 1] = *reinterpret_cast<const uint32_t *>(&hp);
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            *reinterpret_cast<uint4 *>(smem + PX_P + kmaj128(key, hb / 8 + 2 * g + u)) =
+                make_uint4(ph[4 * u], ph[4 * u + 1], ph[4 * u + 2], ph[4 * u + 3]);
         }
-        return over;
+        fence_proxy_async_smem();
+        tc_fence_before();
+        return top;
       };
-      const float over = logits();
       if (begins) {
 #pragma unroll
         for (int h = 0; h < 32; ++h) sum_h[h] = 0.f;
       }
-      if (soft_any(begins || !ok || over > PX_LAG)) {
-        // new references: the maxima so far; O^T and the sums follow (O^T holds nothing yet where a piece begins)
-        red[(warp - 8) * 32 + lane] = reduce_scatter32<true>(reinterpret_cast<float(&)[32]>(s));
+      // P^T is written before it is known whether a reference has to move; it seldom has, except where a piece
+      // begins.  (Once moved the references are the maxima so far: there is no third round.)
+      for (int round = begins ? 0 : 1;; ++round) {
+        const float top = round == 0 ? INFINITY : weights();
+        if (!soft_any(!ok || (round < 2 && top > PX_LAG + PX_BIAS))) break;
+        // new references; O^T and the sums follow (O^T holds nothing yet where a piece begins)
+        tc_ld_32x32b_x32(lanes + PX_TMEM_S + hb, reinterpret_cast<uint32_t(&)[32]>(s));
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float4 q, r;
+          lds_pair(q, r, head + 16 * i);
+          const float qs[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[4 * i + e] = valid ? (s[4 * i + e] * m2.x) * qs[e] : -INFINITY;
+        }
+        red[(warp - 4) * 32 + lane] = reduce_scatter32<true>(s);
         if (soft_any(!ok)) {
           alive = false;
           break;
         }
         const float *rg = red + (hb >> 5) * 128;
-        const float top = fmaxf(fmaxf(rg[lane], rg[32 + lane]), fmaxf(rg[64 + lane], rg[96 + lane]));
-        const float old = begins ? -INFINITY : mr[lane];
-        const float now = fmaxf(old, top);
+        const float most = fmaxf(fmaxf(rg[lane], rg[32 + lane]), fmaxf(rg[64 + lane], rg[96 + lane]));
+        const float old = round == 0 ? -INFINITY : mref[hb + lane];
+        const float now = fmaxf(old, most);
         const float alpha = old == -INFINITY ? 0.f : ex2(old - now);  // lane h: head hb + h
         soft_any(false);  // every warp has read the old references and the maxima
-        if (q4 == 0) mr[lane] = now;
-        if (!begins) {
+        if (q4 == 0) {
+          mref[hb + lane] = now;
+          nref[hb + lane] = PX_BIAS - now;
+        }
+        if (round > 0) {
 #pragma unroll
           for (int h = 0; h < 32; ++h) sum_h[h] *= __shfl_sync(0xffffffffu, alpha, h);
+#pragma unroll 1
           for (int d = 0; d < 4; ++d) {
             uint32_t r[32];
             tc_ld_32x32b_x32(lanes + d * 64 + hb, r);
@@ -438,62 +776,46 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
             tc_st_32x32b_x32(lanes + d * 64 + hb, r);
           }
           tc_wait_st();
+          tc_fence_before();
         }
         soft_any(false);  // the new references are written
-        logits();         // (the reduction above used the registers up)
+        round = 1;
       }
-      begins = false;
-      uint32_t ph[16];
+      if (!alive) break;
+      if (t == 0) mbar_arrive(p_full);
+      const bool ends = w.ends_piece();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 m4 = reinterpret_cast<const float4 *>(mr)[i];
-        const float ms[4] = {m4.x, m4.y, m4.z, m4.w};
-        float e[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          e[u] = valid ? ex2(__uint_as_float(s[4 * i + u]) - (ms[u] - PX_BIAS)) : 0.f;
-          sum_h[4 * i + u] += e[u];
-        }
-        const __half2 h0 = __floats2half2_rn(e[0] * m2.y, e[1] * m2.y), h1 = __floats2half2_rn(e[2] * m2.y, e[3] * m2.y);
-        ph[2 * i] = *reinterpret_cast<const uint32_t *>(&h0);
-        ph[2 * i + 1] = *reinterpret_cast<const uint32_t *>(&h1);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        *reinterpret_cast<uint4 *>(smem + PX_P + kmaj128(key, hb / 8 + u)) =
-            make_uint4(ph[4 * u], ph[4 * u + 1], ph[4 * u + 2], ph[4 * u + 3]);
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
-      if (!w.ends_piece()) {
+      for (int h = 0; h < 32; h += 2) add2(sum_h[h], sum_h[h + 1], s[h], s[h + 1]);
+      begins = ends;
+      if (!ends) {
         w.next(p);
         continue;
       }
-      // ---- the piece's tiles are done: the next piece's query goes out first, then O^T is read
+      // ---- the piece's tiles are done: the next piece begins on the tensor core, then O^T is read
       const int row = w.row;
       // whole, or a part: the row began in an earlier block (slot 0) or only goes on in a later one (slot 1)
       const bool from_start = piece > 0 || first[1] == 0;
       const bool whole = from_start && w.tile + 1 == w.k.tiles;
+      red[(warp - 4) * 32 + lane] = reduce_scatter32<false>(sum_h);
       w.next(p);
       if (w.left > 0) {
-        load_query(p, w.row, smem, qinv + ((piece + 1) & 1) * H, t);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
+        load_query(p, w.row, smem, qmu, t);
+        if (t == 0) mbar_arrive(q_full);
       }
       const bool o_ok = mbar_wait_bounded(o_full, piece & 1, abort_flag, PX_WAIT_NS);
       tc_fence_after();
-      red[(warp - 8) * 32 + lane] = reduce_scatter32<false>(sum_h);
       if (soft_any(!o_ok)) {
         alive = false;
         break;
       }
       const float *rg = red + (hb >> 5) * 128;
-      const float total_h = (rg[lane] + rg[32 + lane]) + (rg[64 + lane] + rg[96 + lane]);
-      const float m = mr[lane];
+      const float total_h = (rg[lane] + rg[32 + lane]) + (rg[64 + lane] + rg[96 + lane]);  // lane h: head hb + h
       float *part = p.parts + (int64_t(blockIdx.x) * 2 + (from_start ? 1 : 0)) * PX_SLOT;
-      const float inv = whole ? (total_h > 0.f ? 1.f / total_h : (total_h == 0.f ? 0.f : total_h)) : 1.f;
+      // 2^7: the tile's values are 2^-7 of the keys'; over the sum where it is whole (0 for no key; NaN stays)
+      const float inv = !whole ? 128.f : total_h > 0.f ? 128.f / total_h : total_h;
+      const int dim = (key & ~7) + ((key & 7) >> 1) + 4 * (key & 1);  // of this lane's O^T row (see dequant128)
       if (q4 == 0) {
+        const float m = mref[hb + lane];
         if (whole) {
           p.lse[int64_t(row) * H + hb + lane] =
               total_h == 0.f ? -INFINITY : (m - PX_BIAS + log2f(total_h)) * 0.69314718055994531f;
@@ -502,85 +824,39 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
           part[PX_PART + H + hb + lane] = total_h;
         }
       }
+#pragma unroll 1
       for (int d = 0; d < 4; ++d) {
-        uint32_t r[32];
-        tc_ld_32x32b_x32(lanes + d * 64 + hb, r);
+        float r[32];
+        tc_ld_32x32b_x32(lanes + d * 64 + hb, reinterpret_cast<uint32_t(&)[32]>(r));
         tc_wait_ld();
-        const int dim = 128 * d + key;
+#pragma unroll
+        for (int h = 0; h < 32; ++h) r[h] *= __shfl_sync(0xffffffffu, inv, h);
         if (whole && p.o_bf16) {
-          uint16_t *orow = static_cast<uint16_t *>(p.o) + (int64_t(row) * H + hb) * D + dim;
+          // lanes l and l ^ 2 hold neighbouring dims: of two heads the first lane stores the one, the second the other
+          const bool second = lane & 2;
+          uint32_t *orow = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) +
+                                                        (int64_t(row) * H + hb + (second ? 1 : 0)) * D + 128 * d + (dim & ~1));
 #pragma unroll
-          for (int h = 0; h < 32; ++h)
-            orow[h * D] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[h]) * __shfl_sync(0xffffffffu, inv, h)));
+          for (int h = 0; h < 32; h += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, second ? r[h] : r[h + 1], 2);
+            const __nv_bfloat162 v = second ? __floats2bfloat162_rn(got, r[h + 1]) : __floats2bfloat162_rn(r[h], got);
+            orow[h * (D / 2)] = *reinterpret_cast<const uint32_t *>(&v);
+          }
         } else {
-          float *orow = whole ? static_cast<float *>(p.o) + (int64_t(row) * H + hb) * D + dim : part + hb * D + dim;
+          float *orow = (whole ? static_cast<float *>(p.o) + (int64_t(row) * H + hb) * D : part + hb * D) + 128 * d + dim;
 #pragma unroll
-          for (int h = 0; h < 32; ++h) orow[h * D] = __uint_as_float(r[h]) * __shfl_sync(0xffffffffu, inv, h);
+          for (int h = 0; h < 32; ++h) orow[h * D] = r[h];
         }
       }
       tc_fence_before();
       soft_any(false);  // the sums and O^T have been read
       ++piece;
-      begins = true;
     }
     if (!alive && t == 0) report(p.err, CSA2_ERR_TIMEOUT);
-  } else {
-    regs_down<PX_REG_ISSUE>();
-  }
-  if (tid == PX_PROD + PX_SOFT) {
-    // ------------------------------------------------------------ the tensor core's issuer
-    const uint32_t kt = smem_u32(smem + PX_K), qt = smem_u32(smem + PX_Q), pt = smem_u32(smem + PX_P);
-    constexpr uint32_t id_s = idesc_f16(PX_TILE, H, false, false), id_o = idesc_f16(PX_TILE, H, true, true);
-    bool begins = true, ok = true;
-    int piece = 0;
-    for (int n = 0; w.left > 0 && ok; ++n) {
-      if (begins) {
-        if (!(ok = mbar_wait_bounded(q_full, piece & 1, abort_flag, PX_WAIT_NS))) break;
-        tc_fence_after();
-      }
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const int d = (i & 1) * 2 + (i >> 1);  // the order in which the producers' halves write them
-        if (!(ok = mbar_wait_bounded(&full[d], n & 1, abort_flag, PX_WAIT_NS))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4)
-            tc_mma_f16(tmem + PX_TMEM_S, smem_desc(kt + (2 * d + c) * 16384 + 32 * k4, 16, 1024, LAYOUT_SWIZZLE_128B),
-                       smem_desc(qt + (2 * d + c) * 8192 + 32 * k4, 16, 1024, LAYOUT_SWIZZLE_128B), id_s,
-                       i > 0 || c > 0 || k4 > 0);
-      }
-      if (!ok) break;
-      tc_commit(s_full);
-      if (!(ok = mbar_wait_bounded(p_full, n & 1, abort_flag, PX_WAIT_NS))) break;
-      tc_fence_after();
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const int d = (i & 1) * 2 + (i >> 1);
-#pragma unroll
-        for (int jc = 0; jc < 2; ++jc)
-#pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4)
-            tc_mma_f16(tmem + d * 64,
-                       smem_desc(kt + (2 * d) * 16384 + jc * 8192 + 2048 * k4, 16384, 1024, LAYOUT_SWIZZLE_128B),
-                       smem_desc(pt + (8 * jc + 2 * k4) * 1024, 16, 1024, LAYOUT_SWIZZLE_128B), id_o,
-                       !begins || jc > 0 || k4 > 0);
-        tc_commit(&freed[d]);
-      }
-      begins = w.ends_piece();
-      if (begins) {
-        tc_commit(o_full);
-        ++piece;
-      }
-      w.next(p);
-    }
-    tc_commit(idle);
-    mbar_wait_bounded(idle, 0, abort_flag, PX_WAIT_NS);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, PX_TMEM_COLS);
   }
@@ -637,11 +913,24 @@ int prefix_blocks(int64_t rows, int max_entries, int most) {
   const int64_t tiles = rows * ((int64_t(max_entries) + 128 + PX_TILE - 1) / PX_TILE);
   return int(tiles < most ? tiles : most);
 }
-size_t plan_bytes(int64_t rows) { return (size_t(rows) * 4 + 68 + 255) & ~size_t(255); }
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// The workspace: the plan, the shared tiles' flags, the partial rows, the shared tiles in fp16.
+struct Layout {
+  int shared;
+  size_t bad, parts, rows16, bytes;
+  Layout(int64_t rows, int entries, int blocks) {
+    shared = rows >= PX_MIN_ROWS ? entries / PX_TILE : 0;
+    bad = round256(size_t(rows + 17) * 4);
+    parts = bad + round256(size_t(shared) * 4);
+    rows16 = parts + round256(size_t(blocks) * 2 * PX_SLOT * 4);
+    bytes = rows16 + size_t(shared) * PX_TILE * D * 2;
+  }
+};
 }  // namespace
 
 size_t prefix_workspace(int64_t rows, int max_entries) {
-  return plan_bytes(rows) + size_t(prefix_blocks(rows, max_entries, PX_MAX_CTAS)) * 2 * PX_SLOT * 4;
+  return Layout(rows, max_entries, prefix_blocks(rows, max_entries, PX_MAX_CTAS)).bytes;
 }
 
 void launch_prefix_attn(const uint16_t *q, int B, int Q, const int32_t *q_pos, float tau, int prefix, int max_entries,
@@ -654,19 +943,32 @@ void launch_prefix_attn(const uint16_t *q, int B, int Q, const int32_t *q_pos, f
   for (a.page_shift = 0; c.page_table && (1 << a.page_shift) < c.page_size;) ++a.page_shift;
   a.codes = codes, a.scale = scale, a.R = R, a.window = window;
   a.o = o, a.o_bf16 = o_bf16, a.lse = lse, a.err = err;
-  a.plan = static_cast<int32_t *>(ws);
-  a.parts = reinterpret_cast<float *>(static_cast<char *>(ws) + plan_bytes(rows));
+  const int sms = sm_count(), blocks = prefix_blocks(rows, max_entries, sms < PX_MAX_CTAS ? sms : PX_MAX_CTAS);
+  const Layout at(rows, prefix < max_entries ? prefix : max_entries, blocks);
+  char *w = static_cast<char *>(ws);
+  a.plan = reinterpret_cast<int32_t *>(w);
+  a.bad = reinterpret_cast<int32_t *>(w + at.bad);
+  a.parts = reinterpret_cast<float *>(w + at.parts);
+  a.rows16 = reinterpret_cast<uint16_t *>(w + at.rows16);
+  CUtensorMap map;
+  memset(&map, 0, sizeof(map));
+  if (at.shared > 0 && make_half_rows_map(&map, a.rows16, int64_t(at.shared) * PX_TILE)) a.shared = at.shared;
   set_smem_limit(prefix_attn_kernel, PX_SMEM);
-  const int sms = sm_count();
-  prefix_attn_kernel<<<prefix_blocks(rows, max_entries, sms < PX_MAX_CTAS ? sms : PX_MAX_CTAS), PX_THREADS, PX_SMEM, st>>>(a);
+  if (a.shared > 0) prefix_expand_kernel<<<a.shared, 256, 0, st>>>(a);
+  cudaLaunchAttribute dependent[1];
+  dependent[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  dependent[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(PX_THREADS);
+  cfg.dynamicSmemBytes = PX_SMEM;
+  cfg.stream = st;
+  cfg.attrs = dependent;
+  cfg.numAttrs = a.shared > 0 ? 1 : 0;  // only behind a kernel of this call
+  cudaLaunchKernelEx(&cfg, prefix_attn_kernel, map, a);
   cfg.gridDim = dim3(rows, H / 8);
   cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
+  cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   cudaLaunchKernelEx(&cfg, prefix_combine_kernel, a);
 }
