@@ -76,7 +76,7 @@ struct PrefixArgs {
   void *o;
   int o_bf16;
   float *lse;
-  int32_t *plan;  // [0] tiles per block; from [16]: first tile of each row, and the number of tiles
+  int32_t *plan;  // [0] tiles per block, or [1] blocks per row; from [16]: first tile of each row, and the number of tiles
   int shared;     // tiles of the prefix that are dequantised ahead (0: none),
   uint16_t *rows16;  // their entries in fp16, 512 each,
   int32_t *bad;      // and per tile whether one of its entries is outside the cache
@@ -102,6 +102,12 @@ __device__ __forceinline__ RowKeys row_keys(const PrefixArgs &p, int row) {
   k.nk = k.nks + nkw;
   k.tiles = (k.nks + nkw + PX_TILE - 1) / PX_TILE;
   return k;
+}
+
+// First tile of part i of a row of n tiles in at most `parts` parts (fewer where it has fewer tiles).
+__device__ __forceinline__ int part_start(int n, int i, int parts) {
+  const int m = min(n, parts);
+  return i < m ? int(int64_t(n) * i / m) : n;
 }
 
 // A block's tiles in order: tile `tile` of row `row`, `left` tiles to go with it.
@@ -473,39 +479,56 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   volatile int *abort_flag = reinterpret_cast<volatile int *>(s_full + 6);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
-  // ---- the plan: all rows' tiles, the tiles per block, and where this block's begin
-  int sum = 0;
+  // ---- the plan: the tiles of all rows and of the longest, and this block's share
+  int *first = scan + 36;  // this block's first row, first tile of it, shared tiles, longest row
+  int sum = 0, most = 0;
   for (int row = tid; row < p.rows; row += PX_THREADS) {
-    sum += row_keys(p, row).tiles;
+    const int n = row_keys(p, row).tiles;
+    sum += n;
+    most = max(most, n);
     if (blockIdx.x == 0 && visible_entries(p.c, row / p.Q, p.q_pos[row]) > p.n_bound) report(p.err, CSA2_ERR_SHAPE);
   }
+  if (tid == 0) first[3] = 0;
   int total = 0;
   block_exclusive_scan_1024(sum, scan, &total);
-  const int per = max(1, (total + int(gridDim.x) - 1) / int(gridDim.x));
-  const int t0 = blockIdx.x * per, t1 = min(total, t0 + per);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) atomicMax(&first[3], most);
+  __syncthreads();
+  // Equal shares of all tiles in row order; or, where that makes no block's share more than an eighth longer, each row
+  // in as many equal parts as there are blocks for it.  Rows of equal length then pass over the prefix side by side, and
+  // what one of them has read is still in L2 for the others (16 rows over 65536 entries: see the file's head).
+  const int per = max(1, (total + int(gridDim.x) - 1) / int(gridDim.x)), parts = int(gridDim.x) / p.rows;
+  const bool by_row = parts > 0 && 8 * ((first[3] + parts - 1) / max(parts, 1)) <= 9 * per;
   if (blockIdx.x == 0 && tid == 0) {
     p.plan[0] = per;
+    p.plan[1] = by_row ? parts : 0;
     p.plan[16 + p.rows] = total;
   }
-  if (t0 >= t1 && blockIdx.x != 0) return;
-  int *first = scan + 36;
-  for (int row0 = 0, base = 0; row0 < p.rows; row0 += PX_THREADS) {
-    const int row = row0 + tid;
-    const int n = row < p.rows ? row_keys(p, row).tiles : 0;
-    int all = 0;
-    const int off = base + block_exclusive_scan_1024(n, scan, &all);
-    if (blockIdx.x == 0 && row < p.rows) p.plan[16 + row] = off;
-    if (n > 0 && off <= t0 && t0 < off + n) {
-      first[0] = row;
-      first[1] = t0 - off;
-    }
-    base += all;
-    if (blockIdx.x != 0 && t0 < base) break;
+  int t0 = blockIdx.x * per, t1 = min(total, t0 + per);
+  if (by_row) {
+    const int row = blockIdx.x / parts, i = blockIdx.x % parts, n = row < p.rows ? row_keys(p, row).tiles : 0;
+    t0 = part_start(n, i, parts), t1 = part_start(n, i + 1, parts);
+    if (tid == 0) first[0] = row, first[1] = t0;
   }
+  if (t0 >= t1 && blockIdx.x != 0) return;
+  if (!by_row || blockIdx.x == 0)
+    for (int row0 = 0, base = 0; row0 < p.rows; row0 += PX_THREADS) {
+      const int row = row0 + tid;
+      const int n = row < p.rows ? row_keys(p, row).tiles : 0;
+      int all = 0;
+      const int off = base + block_exclusive_scan_1024(n, scan, &all);
+      if (blockIdx.x == 0 && row < p.rows) p.plan[16 + row] = off;
+      if (!by_row && n > 0 && off <= t0 && t0 < off + n) {
+        first[0] = row;
+        first[1] = t0 - off;
+      }
+      base += all;
+      if (blockIdx.x != 0 && t0 < base) break;
+    }
   grid_dep_launch();
   if (t0 >= t1) return;
   // entries below `limit` are read from the workspace: the shared tiles before the first bad one
-  int *limit_at = scan + 38;
+  int *limit_at = first + 2;
   if (tid == 0) *limit_at = p.shared;
   grid_dep_wait();
   __syncthreads();
@@ -602,8 +625,8 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
           if (last[d] >= 0) mbar_wait_bounded(&full[d], last[d] & 1, &never, PX_WAIT_NS);
     }
     // ------------------------------------------------------------ the tensor core's issuer
-    // O^T += V^T P^T for the 128 dims of a pair of blocks, and S^T of the next tile over them as soon as they are
-    // written, some steps behind their last use.
+    // O^T += V^T P^T, 128 dims (a pair of blocks) at a time, then S^T of the next tile over each pair as soon as it is
+    // written, four steps behind its last use.
     if (warp == PX_ISSUE_WARP) {
       const uint32_t kt = smem_u32(smem + PX_K), qt = smem_u32(smem + PX_Q), pt = smem_u32(smem + PX_P);
       const uint32_t leader = elect_one();
@@ -641,16 +664,13 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
         }
         const bool ends = w.ends_piece();
         if (!wait(p_full, n)) break;
-        step_o(0, begins);
-        step_o(1, begins);
-        step_o(2, begins);
-        if (!ends && !step_s(n + 1, 0, true)) break;
-        step_o(3, begins);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) step_o(d, begins);
         if (ends) {
           commit_to(leader, o_full);
           ++piece;
         } else {
-          if (!step_s(n + 1, 1, false) || !step_s(n + 1, 2, false) || !step_s(n + 1, 3, false)) break;
+          if (!step_s(n + 1, 0, true) || !step_s(n + 1, 1, false) || !step_s(n + 1, 2, false) || !step_s(n + 1, 3, false)) break;
           commit_to(leader, s_full);
         }
         w.next(p);
@@ -869,8 +889,10 @@ __global__ void __launch_bounds__(256) prefix_combine_kernel(const __grid_consta
   __shared__ float inv[8];
   grid_dep_wait();
   const int row = blockIdx.x, h0 = 8 * blockIdx.y, t = threadIdx.x;
-  const int a = p.plan[16 + row], b = p.plan[17 + row], per = p.plan[0];
-  const int c0 = a / per, n = b > a ? (b - 1) / per - c0 + 1 : 0;
+  const int a = p.plan[16 + row], b = p.plan[17 + row], per = p.plan[0], by_row = p.plan[1];
+  // the blocks that hold a part of the row: c0 .. c0 + n - 1
+  const int c0 = by_row ? row * by_row : a / per;
+  const int n = by_row ? min(by_row, b - a) : (b > a ? (b - 1) / per - c0 + 1 : 0);
   if (n == 1) return;
   // the first block holds the row's start as its last piece (slot 1), the others as their first (slot 0)
   auto part = [&](int i) { return p.parts + (int64_t(c0 + i) * 2 + (i == 0 ? 1 : 0)) * PX_SLOT; };
