@@ -15,7 +15,7 @@
 //   the key tile       128 KB of shared memory, 8 blocks of 64 dims, 128-byte swizzle: the K-major A operand of
 //                      S^T = K Q^T and, the same bytes, the MN-major A operand of O^T += V^T P^T; written by
 //   1 loading warp     (shared tiles, TMA) or by
-//   4 producer warps   (the others), a pair of blocks as soon as the previous tile's products have read it;
+//   8 producer warps   (the others), a pair of blocks as soon as the previous tile's products have read it;
 //   1 issuing warp     32 + 32 tcgen05.mma of 128 x 64 x 16 (M = keys or dims, N = the 64 heads); O^T stays in
 //                      TMEM (4 x 64 columns) over all tiles of a row;
 //   8 softmax warps    read S^T (a lane is a key, a register a head), exponentiate and write P^T in fp16.
@@ -35,12 +35,12 @@ using namespace sm100;
 
 namespace {
 constexpr int PX_TILE = 128;                 // keys per tile
-constexpr int PX_PROD = 128, PX_SOFT = 256;  // producer and softmax threads (warps 0-3, 4-11)
-constexpr int PX_ISSUE_WARP = 12, PX_LOAD_WARP = 13;
+constexpr int PX_PROD = 256, PX_SOFT = 256;  // producer and softmax threads (warps 0-7, 8-15)
+constexpr int PX_ISSUE_WARP = 16, PX_LOAD_WARP = 17;
 constexpr int PX_THREADS = PX_PROD + PX_SOFT + 128;  // (the last warpgroup has two working warps)
-// Registers per thread after launch (128 x 512): 128 x 128 + 256 x 152 + 128 x 72 = 64512.
-constexpr int PX_REG_SOFT = 152, PX_REG_ISSUE = 72;
-static_assert(PX_PROD * 128 + PX_SOFT * PX_REG_SOFT + 128 * PX_REG_ISSUE <= 128 * PX_THREADS,
+// Registers per thread after launch (96 x 640): 256 x 96 + 256 x 120 + 128 x 48 = 61440.
+constexpr int PX_REG_SOFT = 120, PX_REG_ISSUE = 48;
+static_assert(PX_PROD * 96 + PX_SOFT * PX_REG_SOFT + 128 * PX_REG_ISSUE <= 96 * PX_THREADS,
               "the warpgroups' registers exceed the block's");
 constexpr int PX_MIN_ROWS = 4;               // rows from which a shared prefix is dequantised ahead
 constexpr int PX_MAX_CTAS = 160;             // workspace is sized for at most this many blocks
@@ -55,7 +55,8 @@ constexpr int PX_MUL = PX_P + 16384;              // [2][128] logit and weight m
 constexpr int PX_HEAD = PX_MUL + 2 * 128 * 8;     // per head: [64] logit factors, references, negated references
 constexpr int PX_RED = PX_HEAD + 3 * 64 * 4;      // [8 warps][32]
 constexpr int PX_QMX = PX_RED + 8 * 32 * 4;       // [8 warps][16] query maxima
-constexpr int PX_SCAN = PX_QMX + 8 * 16 * 4;      // 40 ints
+constexpr int PX_INV = PX_QMX + 8 * 16 * 4;       // [64]
+constexpr int PX_SCAN = PX_INV + 64 * 4;          // 40 ints
 constexpr int PX_BAR = PX_SCAN + 40 * 4;
 constexpr int PX_SMEM = PX_BAR + 16 * 8 + 1024;
 static_assert(PX_SMEM <= 227 * 1024, "prefix attention exceeds the shared memory of a block");
@@ -79,7 +80,7 @@ struct PrefixArgs {
   int32_t *plan;  // [0] tiles per block, or [1] blocks per row; from [16]: first tile of each row, and the number of tiles
   int shared;     // tiles of the prefix that are dequantised ahead (0: none),
   uint16_t *rows16;  // their entries in fp16, 512 each,
-  int32_t *bad;      // and per tile whether one of its entries is outside the cache
+  int32_t *bad;      // and for each 32 of them whether one is outside the cache
   float *parts;   // two slots of PX_SLOT floats per block
   int32_t *err;
 };
@@ -104,9 +105,11 @@ __device__ __forceinline__ RowKeys row_keys(const PrefixArgs &p, int row) {
   return k;
 }
 
-// First tile of part i of a row of n tiles in at most `parts` parts (fewer where it has fewer tiles).
+// A row of n tiles in at most `parts` parts: no part of fewer than two tiles (joining a partial row costs about what
+// a tile does); and the first tile of part i.
+__device__ __forceinline__ int part_count(int n, int parts) { return min((n + 1) / 2, parts); }
 __device__ __forceinline__ int part_start(int n, int i, int parts) {
-  const int m = min(n, parts);
+  const int m = part_count(n, parts);
   return i < m ? int(int64_t(n) * i / m) : n;
 }
 
@@ -156,83 +159,39 @@ __device__ __forceinline__ void unpack8(uint32_t w, uint32_t s128, uint32_t *o) 
 // 2^7 times an E4M3 scale, in both halves (at most 57344).
 __device__ __forceinline__ uint32_t scale128(uint32_t byte) { return hmul2_u32(cvt_e4m3x2_f16x2(byte * 0x101u), 0x58005800u); }
 
-// The prefix's complete tiles in fp16, one block each.  Memory bound: 288 bytes read and 1 KB written an entry.
+// The prefix's complete tiles in fp16, 32 entries a block, four a warp.  Memory bound: 288 bytes read and 1 KB
+// written an entry.
+constexpr int EXPAND = 32;
 __global__ void __launch_bounds__(256) prefix_expand_kernel(const __grid_constant__ PrefixArgs p) {
   grid_dep_launch();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j0 = blockIdx.x * PX_TILE + 16 * warp;
-  const uint32_t mine = lane < 16 ? entry_slot(p, 0, j0 + lane, entry_page(p, 0, j0 + lane)) : 0u;
+  const int lane = threadIdx.x & 31, j0 = blockIdx.x * EXPAND + 4 * (threadIdx.x >> 5);
+  int32_t page[4];
+  uint32_t slot[4], sc[4];
+  uint2 codes[4];
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    uint2 codes[4];
-    uint32_t sc[4], slot[4];
+  for (int i = 0; i < 4; ++i) page[i] = entry_page(p, 0, j0 + i);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      slot[i] = __shfl_sync(0xffffffffu, mine, 4 * g + i);
-      codes[i] = make_uint2(0u, 0u);
-      sc[i] = 0u;
-      if (slot[i] != NO_SLOT) {
-        codes[i] = reinterpret_cast<const uint2 *>(p.c.kv_codes + int64_t(slot[i]) * CSA2_MAIN_CODE_BYTES)[lane];
-        sc[i] = p.c.kv_scales[int64_t(slot[i]) * CSA2_MAIN_SCALE_BYTES + lane];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t h[8];
-      const uint32_t s = scale128(sc[i]);
-      unpack8(codes[i].x, s, h);
-      unpack8(codes[i].y, s, h + 4);
-      uint4 *o = reinterpret_cast<uint4 *>(p.rows16 + int64_t(j0 + 4 * g + i) * D) + 2 * lane;
-      o[0] = make_uint4(h[0], h[1], h[2], h[3]);
-      o[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  for (int i = 0; i < 4; ++i) {
+    slot[i] = entry_slot(p, 0, j0 + i, page[i]);
+    codes[i] = make_uint2(0u, 0u);
+    sc[i] = 0u;
+    if (slot[i] != NO_SLOT) {
+      codes[i] = reinterpret_cast<const uint2 *>(p.c.kv_codes + int64_t(slot[i]) * CSA2_MAIN_CODE_BYTES)[lane];
+      sc[i] = p.c.kv_scales[int64_t(slot[i]) * CSA2_MAIN_SCALE_BYTES + lane];
     }
   }
-  const int any = __syncthreads_or(mine == NO_SLOT);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h[8];
+    const uint32_t s = scale128(sc[i]);
+    unpack8(codes[i].x, s, h);
+    unpack8(codes[i].y, s, h + 4);
+    uint4 *o = reinterpret_cast<uint4 *>(p.rows16 + int64_t(j0 + i) * D) + 2 * lane;
+    o[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    o[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+  const int any = __syncthreads_or(slot[0] == NO_SLOT || slot[1] == NO_SLOT || slot[2] == NO_SLOT || slot[3] == NO_SLOT);
   if (threadIdx.x == 0) p.bad[blockIdx.x] = any;
-}
-
-// A producer thread's part of a tile: 32 dims of each pair of blocks, of four keys 8 apart.  A warp's load of 16 bytes
-// a thread covers 64 bytes of each of eight keys, and its 16-byte stores fall into all banks.
-struct KeyPart {
-  uint32_t slot[4];  // cache slot of an entry, ring slot of a window token; NO_SLOT: no key
-  int entries;       // keys of the tile below this are entries
-  uint4 raw[4];      // entries' codes in one pair of blocks
-  uint32_t sc[4];    // and their two scales
-};
-struct KeyPlace {
-  int key0;   // the first of its keys
-  int piece;  // which 32 dims of the pair
-};
-
-// The slots of the tile's keys.
-__device__ __forceinline__ void find_keys(const PrefixArgs &p, const Work &w, const KeyPlace &at, KeyPart &r) {
-  r.entries = w.k.nks - w.tile * PX_TILE;
-  int32_t page[4];  // (the four table entries are fetched together)
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int j = w.tile * PX_TILE + at.key0 + 8 * i;
-    page[i] = j < w.k.nks ? entry_page(p, j < p.prefix ? 0 : w.k.b, j) : -1;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int j = w.tile * PX_TILE + at.key0 + 8 * i;
-    r.slot[i] = j < w.k.nks ? entry_slot(p, j < p.prefix ? 0 : w.k.b, j, page[i]) : NO_SLOT;
-    if (j >= w.k.nks && j < w.k.nk) r.slot[i] = uint32_t(w.k.b) * p.R + (w.k.lo + (j - w.k.nks)) % p.R;
-  }
-  if (at.piece == 0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (r.slot[i] == NO_SLOT && at.key0 + 8 * i < r.entries) report(p.err, CSA2_ERR_INDEX);
-  }
-}
-
-// The entries' codes and scales of pair d.
-__device__ __forceinline__ void load_keys(const PrefixArgs &p, const KeyPlace &at, int d, KeyPart &r) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (at.key0 + 8 * i < r.entries && r.slot[i] != NO_SLOT) {
-      r.raw[i] = *reinterpret_cast<const uint4 *>(p.c.kv_codes + int64_t(r.slot[i]) * CSA2_MAIN_CODE_BYTES + 64 * d + at.piece * 16);
-      r.sc[i] = *reinterpret_cast<const uint16_t *>(p.c.kv_scales + int64_t(r.slot[i]) * CSA2_MAIN_SCALE_BYTES + 8 * d + at.piece * 2);
-    }
 }
 
 // A window token's scale as 2^k f: 2^(k - 7) goes into the fp16 values, f into the logit and the weight.  Codes
@@ -242,44 +201,89 @@ __device__ __forceinline__ int window_exponent(float scale) {
   return max(-16, min(14, int((__float_as_uint(scale) >> 23) & 255) - 127));
 }
 
-// The factors of the logits and weights of the tile's keys (NaN: no key).
-__device__ __forceinline__ void store_factors(const PrefixArgs &p, const KeyPlace &at, const KeyPart &r, float2 *mul) {
+// A producer thread's part of a tile: 32 dims of each pair of blocks, of two keys 8 apart.  A warp's load of 16 bytes
+// a thread covers 64 bytes of each of eight keys, and its 16-byte stores fall into all banks.
+struct KeyPart {
+  uint32_t slot[2];  // cache slot of an entry, ring slot of a window token; NO_SLOT: no key
+  int entries;       // keys of the tile below this are entries
+  float scale[2];    // a window token's scale
+  uint4 raw[2][2];   // in one pair of blocks, an entry's 32 codes [0] and two scales [1].x, or a token's 32 codes
+};
+struct KeyPlace {
+  int key0;   // the first of its keys
+  int piece;  // which 32 dims of the pair
+};
+
+// The slots of the tile's keys.
+__device__ __forceinline__ void find_keys(const PrefixArgs &p, const Work &w, const KeyPlace &at, KeyPart &r) {
+  r.entries = w.k.nks - w.tile * PX_TILE;
+  int32_t page[2];  // (the two table entries are fetched together)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int key = at.key0 + 8 * i;
-    float f = __int_as_float(0x7FFFFFFF);
-    if (r.slot[i] != NO_SLOT) {
-      f = 1.f;
-      if (key >= r.entries) {
-        const float sc = p.scale[r.slot[i]];
-        f = sc * pow2f(-window_exponent(sc));
-      }
+  for (int i = 0; i < 2; ++i) {
+    const int j = w.tile * PX_TILE + at.key0 + 8 * i;
+    page[i] = j < w.k.nks ? entry_page(p, j < p.prefix ? 0 : w.k.b, j) : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = w.tile * PX_TILE + at.key0 + 8 * i;
+    r.slot[i] = j < w.k.nks ? entry_slot(p, j < p.prefix ? 0 : w.k.b, j, page[i]) : NO_SLOT;
+    if (j >= w.k.nks && j < w.k.nk) {
+      r.slot[i] = uint32_t(w.k.b) * p.R + (w.k.lo + (j - w.k.nks)) % p.R;
+      r.scale[i] = p.scale[r.slot[i]];
     }
-    mul[key] = make_float2(f, r.slot[i] != NO_SLOT ? f : 0.f);
+  }
+  if (at.piece == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (r.slot[i] == NO_SLOT && at.key0 + 8 * i < r.entries) report(p.err, CSA2_ERR_INDEX);
   }
 }
 
-// Dims 128 d + 32 piece .. + 31 of keys I and I + 1 in fp16, times 2^-7, in the order of unpack8.
-template <int I>
-__device__ __forceinline__ void dequant_keys(const PrefixArgs &p, const KeyPlace &at, const KeyPart &r, int d, uint32_t (&h)[32]) {
+// The keys' bytes of pair d.
+__device__ __forceinline__ void load_keys(const PrefixArgs &p, const KeyPlace &at, int d, KeyPart &r) {
 #pragma unroll
-  for (int i = I; i < I + 2; ++i) {
-    uint32_t *hk = h + 16 * (i - I);
+  for (int i = 0; i < 2; ++i) {
+    if (r.slot[i] == NO_SLOT) continue;
+    if (at.key0 + 8 * i < r.entries) {
+      r.raw[i][0] = *reinterpret_cast<const uint4 *>(p.c.kv_codes + int64_t(r.slot[i]) * CSA2_MAIN_CODE_BYTES + 64 * d + at.piece * 16);
+      r.raw[i][1].x = *reinterpret_cast<const uint16_t *>(p.c.kv_scales + int64_t(r.slot[i]) * CSA2_MAIN_SCALE_BYTES + 8 * d + at.piece * 2);
+    } else {
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.codes + int64_t(r.slot[i]) * CSA2_SWA_DIM + 128 * d + 32 * at.piece);
+      r.raw[i][0] = src[0];
+      r.raw[i][1] = src[1];
+    }
+  }
+}
+
+// The factors of the logits and weights of the tile's keys (NaN: no key).
+__device__ __forceinline__ void store_factors(const KeyPlace &at, const KeyPart &r, float2 *mul) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float f = __int_as_float(0x7FFFFFFF);
+    if (r.slot[i] != NO_SLOT)
+      f = at.key0 + 8 * i < r.entries ? 1.f : r.scale[i] * pow2f(-window_exponent(r.scale[i]));
+    mul[at.key0 + 8 * i] = make_float2(f, r.slot[i] != NO_SLOT ? f : 0.f);
+  }
+}
+
+// Those 32 dims of the keys in fp16, times 2^-7, in the order of unpack8.
+__device__ __forceinline__ void dequant_keys(const KeyPlace &at, const KeyPart &r, uint32_t (&h)[32]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t *hk = h + 16 * i;
+    const uint4 a = r.raw[i][0], b = r.raw[i][1];
     if (r.slot[i] == NO_SLOT) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) hk[e] = 0u;
     } else if (at.key0 + 8 * i < r.entries) {
-      const uint32_t s0 = scale128(r.sc[i] & 0xFFu), s1 = scale128(r.sc[i] >> 8);
-      unpack8(r.raw[i].x, s0, hk);
-      unpack8(r.raw[i].y, s0, hk + 4);
-      unpack8(r.raw[i].z, s1, hk + 8);
-      unpack8(r.raw[i].w, s1, hk + 12);
+      const uint32_t s0 = scale128(b.x & 0xFFu), s1 = scale128(b.x >> 8);
+      unpack8(a.x, s0, hk);
+      unpack8(a.y, s0, hk + 4);
+      unpack8(a.z, s1, hk + 8);
+      unpack8(a.w, s1, hk + 12);
     } else {
-      const __half2 two = __float2half2_rn(pow2f(window_exponent(p.scale[r.slot[i]]) - 7));
+      const __half2 two = __float2half2_rn(pow2f(window_exponent(r.scale[i]) - 7));
       const uint32_t s = *reinterpret_cast<const uint32_t *>(&two);
-      const uint4 *src =
-          reinterpret_cast<const uint4 *>(p.codes + int64_t(r.slot[i]) * CSA2_SWA_DIM + 128 * d + 32 * at.piece);
-      const uint4 a = src[0], b = src[1];
       const uint32_t w8[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int v = 0; v < 4; ++v)
@@ -291,13 +295,12 @@ __device__ __forceinline__ void dequant_keys(const PrefixArgs &p, const KeyPlace
 }
 
 // Those values into the pair of blocks at dst.
-template <int I>
 __device__ __forceinline__ void store_keys(const uint32_t (&h)[32], const KeyPlace &at, uint8_t *dst) {
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int v = 0; v < 4; ++v)
-      *reinterpret_cast<uint4 *>(dst + (at.piece >> 1) * 16384 + kmaj128(at.key0 + 8 * (I + i), 4 * (at.piece & 1) + v)) =
+      *reinterpret_cast<uint4 *>(dst + (at.piece >> 1) * 16384 + kmaj128(at.key0 + 8 * i, 4 * (at.piece & 1) + v)) =
           make_uint4(h[16 * i + 4 * v], h[16 * i + 4 * v + 1], h[16 * i + 4 * v + 2], h[16 * i + 4 * v + 3]);
 }
 
@@ -305,7 +308,7 @@ __device__ __forceinline__ void store_keys(const uint32_t (&h)[32], const KeyPla
 __device__ __forceinline__ bool prod_any(bool pred) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"(uint32_t(pred))
       : "memory");
@@ -416,44 +419,33 @@ __device__ __forceinline__ void load_query(const PrefixArgs &p, int row, uint8_t
   uint32_t *qmx = reinterpret_cast<uint32_t *>(smem + PX_QMX);
   const uint4 *src = reinterpret_cast<const uint4 *>(p.q + int64_t(row) * H * D);
   const int warp = t >> 5, pair = warp & ~1;  // the two warps that hold the heads t / 64 + 4 u
-  uint4 v[8];  // chunk t + 256 u: head t / 64 + 4 u, dims 8 (t % 64) ..; u = 8 half ..
-  auto load = [&](int half) {
+  uint4 v[16];  // chunk t + 256 u: head t / 64 + 4 u, dims 8 (t % 64) ..
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = src[t + 256 * (8 * half + u)];
-  };
+  for (int u = 0; u < 16; ++u) v[u] = src[t + 256 * u];
 #pragma unroll
-  for (int half = 1; half >= 0; --half) {
-    load(half);
+  for (int u = 0; u < 16; ++u) {
+    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+    uint32_t mb = 0;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-      uint32_t mb = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mb = max(mb, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-      mb = __reduce_max_sync(0xffffffffu, mb);
-      if ((t & 31) == 0) qmx[warp * 16 + 8 * half + u] = mb;
-    }
+    for (int i = 0; i < 4; ++i) mb = max(mb, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+    mb = __reduce_max_sync(0xffffffffu, mb);
+    if ((t & 31) == 0) qmx[warp * 16 + u] = mb;
   }
   soft_any(false);
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    if (half) load(half);  // (read twice: 16 chunks do not fit the registers beside the sums)
+  for (int u = 0; u < 16; ++u) {
+    const float sc = pow2f(query_prescale_exp(max(qmx[pair * 16 + u], qmx[pair * 16 + 16 + u])));
+    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+    uint32_t o4[4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int c = 8 * half + u;
-      const float sc = pow2f(query_prescale_exp(max(qmx[pair * 16 + c], qmx[pair * 16 + 16 + c])));
-      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-      uint32_t o4[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {  // dims i and i + 4 of the eight
-        const uint32_t lo = w[i >> 1], hi = w[2 + (i >> 1)];
-        const __half2 hv = __floats2half2_rn(__uint_as_float((i & 1) ? lo & 0xFFFF0000u : lo << 16) * sc,
-                                             __uint_as_float((i & 1) ? hi & 0xFFFF0000u : hi << 16) * sc);
-        o4[i] = *reinterpret_cast<const uint32_t *>(&hv);
-      }
-      const int h = (t >> 6) + 4 * c, u8 = t & 63;
-      *reinterpret_cast<uint4 *>(smem + PX_Q + (u8 / 8) * 8192 + kmaj128(h, u8 % 8)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+    for (int i = 0; i < 4; ++i) {  // dims i and i + 4 of the eight
+      const uint32_t lo = w[i >> 1], hi = w[2 + (i >> 1)];
+      const __half2 hv = __floats2half2_rn(__uint_as_float((i & 1) ? lo & 0xFFFF0000u : lo << 16) * sc,
+                                           __uint_as_float((i & 1) ? hi & 0xFFFF0000u : hi << 16) * sc);
+      o4[i] = *reinterpret_cast<const uint32_t *>(&hv);
     }
+    const int h = (t >> 6) + 4 * u, u8 = t & 63;
+    *reinterpret_cast<uint4 *>(smem + PX_Q + (u8 / 8) * 8192 + kmaj128(h, u8 % 8)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
   }
   if (t < H) {
     const int c = t & 3, u = t >> 2;
@@ -471,6 +463,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   float *qmu = reinterpret_cast<float *>(smem + PX_HEAD);  // logit factor of each head
   float *mref = qmu + H, *nref = mref + H;                 // reference m, and BIAS - m
   float *red = reinterpret_cast<float *>(smem + PX_RED);
+  float *oinv = reinterpret_cast<float *>(smem + PX_INV);  // [64] what a finished row is multiplied by
   int *scan = reinterpret_cast<int *>(smem + PX_SCAN);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + PX_BAR);  // [4] pair of blocks written
   uint64_t *freed = full + 4;                                    // [4] pair of blocks consumed
@@ -498,7 +491,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   // in as many equal parts as there are blocks for it.  Rows of equal length then pass over the prefix side by side, and
   // what one of them has read is still in L2 for the others (16 rows over 65536 entries: see the file's head).
   const int per = max(1, (total + int(gridDim.x) - 1) / int(gridDim.x)), parts = int(gridDim.x) / p.rows;
-  const bool by_row = parts > 0 && 8 * ((first[3] + parts - 1) / max(parts, 1)) <= 9 * per;
+  const bool by_row = parts > 0 && 8 * ((first[3] + parts - 1) / max(parts, 1)) <= 9 * max(per, 2);
   if (blockIdx.x == 0 && tid == 0) {
     p.plan[0] = per;
     p.plan[1] = by_row ? parts : 0;
@@ -532,8 +525,8 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   if (tid == 0) *limit_at = p.shared;
   grid_dep_wait();
   __syncthreads();
-  for (int i = tid; i < p.shared; i += PX_THREADS)
-    if (p.bad[i]) atomicMin(limit_at, i);
+  for (int i = tid; i < p.shared * (PX_TILE / EXPAND); i += PX_THREADS)
+    if (p.bad[i]) atomicMin(limit_at, i / (PX_TILE / EXPAND));
   if (warp == 0) {
     tmem_alloc(tmem_slot, PX_TMEM_COLS);
     tmem_relinquish();
@@ -560,40 +553,37 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   w.k = row_keys(p, w.row);
   const int limit = *limit_at * PX_TILE;
 
-  if (warp < 4) {
-    // ------------------------------------------------------------ producers: warp w keys 32 w .. + 31
-    // Half of each piece is dequantised into registers before its blocks are free, so that little lies between
-    // the last product that reads a block and the first that reads its successor.
-    const KeyPlace at{32 * warp + (lane & 3) + 4 * ((lane >> 3) & 1), ((lane >> 2) & 1) + 2 * (lane >> 4)};
+  if (warp < 8) {
+    // ------------------------------------------------------------ producers: warp w keys 16 w .. + 15
+    // Each pair's values are dequantised into registers, and the next pair's bytes asked for, before the pair's blocks are
+    // free: only the stores lie between the last product that reads a block and the first that reads its successor.
+    const KeyPlace at{16 * warp + (lane & 3) + 4 * ((lane >> 3) & 1), ((lane >> 2) & 1) + 2 * (lane >> 4)};
     KeyPart r;
     uint32_t h[32];
     bool ok = true;
+    int seen = -1;  // the last tile whose products are known to have read it all
     for (int n = 0; w.left > 0 && ok; ++n, w.next(p)) {
-      if (w.within(limit)) {  // not theirs; but a barrier's parity tells only its last two phases apart
-        ok = n == 0 || mbar_wait_bounded(&freed[3], (n - 1) & 1, abort_flag, PX_WAIT_NS);
-        ok = !prod_any(!ok);
-        continue;
-      }
+      if (w.within(limit)) continue;
       find_keys(p, w, at, r);
       load_keys(p, at, 0, r);
 #pragma unroll 1
       for (int d = 0; d < 4; ++d) {
-        uint8_t *dst = smem + PX_K + d * 2 * 16384;
-        dequant_keys<0>(p, at, r, d, h);
-        ok = n == 0 || mbar_wait_bounded(&freed[d], (n - 1) & 1, abort_flag, PX_WAIT_NS);
+        dequant_keys(at, r, h);
+        if (d < 3) load_keys(p, at, d + 1, r);
+        // (a barrier's parity tells only its last two phases apart: the loader's tiles in between are counted too)
+        for (; ok && seen < n - 2; ++seen) ok = mbar_wait_bounded(&freed[3], (seen + 1) & 1, abort_flag, PX_WAIT_NS);
+        if (ok && n > 0) ok = mbar_wait_bounded(&freed[d], (n - 1) & 1, abort_flag, PX_WAIT_NS);
         if (prod_any(!ok)) {
           ok = false;
           break;
         }
-        if (d == 0 && at.piece == 0) store_factors(p, at, r, mul + (n & 1) * 128);
-        store_keys<0>(h, at, dst);
-        dequant_keys<2>(p, at, r, d, h);
-        if (d < 3) load_keys(p, at, d + 1, r);
-        store_keys<2>(h, at, dst);
+        if (d == 0 && at.piece == 0) store_factors(at, r, mul + (n & 1) * 128);
+        store_keys(h, at, smem + PX_K + d * 2 * 16384);
         fence_proxy_async_smem();
         prod_any(false);
         if (tid == 0) mbar_arrive(&full[d]);
       }
+      seen = n - 1;
     }
   } else if (warp >= PX_ISSUE_WARP) {
     regs_down<PX_REG_ISSUE>();
@@ -602,15 +592,16 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
       const uint32_t leader = elect_one(), kt = smem_u32(smem + PX_K);
       if (p.shared > 0) asm volatile("fence.proxy.async;" ::: "memory");  // (the expansion's stores were generic ones)
       bool ok = true;
-      int last[4] = {-1, -1, -1, -1}, never = 0;
+      int last[4] = {-1, -1, -1, -1}, never = 0, seen = -1;
+      auto wait = [&](int d, int n) {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(&freed[d], n & 1, abort_flag, PX_WAIT_NS));
+      };
       for (int n = 0; w.left > 0 && ok; ++n, w.next(p)) {
-        if (!w.within(limit)) {  // (as above)
-          if (n > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&freed[3], (n - 1) & 1, abort_flag, PX_WAIT_NS));
-          continue;
-        }
+        if (!w.within(limit)) continue;
+        for (; ok && seen < n - 2; ++seen) ok = wait(3, seen + 1);  // (as the producers)
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&freed[d], (n - 1) & 1, abort_flag, PX_WAIT_NS));
+          if (ok && n > 0) ok = wait(d, n - 1);
           if (ok) last[d] = n;
           if (ok && leader) {
             mbar_arrive_expect_tx(&full[d], 2 * 16384);
@@ -619,6 +610,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
           }
           __syncwarp();
         }
+        seen = n - 1;
       }
       if (!ok)  // given up: the copies under way still have to land before the block ends
         for (int d = 0; d < 4; ++d)
@@ -686,9 +678,11 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   } else {
     // ------------------------------------------------------------ softmax
     regs_up<PX_REG_SOFT>();
-    const int t = tid - PX_PROD, q4 = warp & 3, hb = 32 * ((warp - 4) >> 2), key = 32 * q4 + lane;
+    const int t = tid - PX_PROD, q4 = warp & 3, hb = 32 * ((warp - 8) >> 2), key = 32 * q4 + lane;
     const uint32_t lanes = tmem + (uint32_t(32 * q4) << 16), head = smem_u32(qmu + hb);
     float sum_h[32];
+#pragma unroll
+    for (int h = 0; h < 32; ++h) sum_h[h] = 0.f;
     int piece = 0;
     bool begins = true, alive = true;
     load_query(p, w.row, smem, qmu, t);
@@ -748,10 +742,6 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
         tc_fence_before();
         return top;
       };
-      if (begins) {
-#pragma unroll
-        for (int h = 0; h < 32; ++h) sum_h[h] = 0.f;
-      }
       // P^T is written before it is known whether a reference has to move; it seldom has, except where a piece
       // begins.  (Once moved the references are the maxima so far: there is no third round.)
       for (int round = begins ? 0 : 1;; ++round) {
@@ -768,7 +758,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[4 * i + e] = valid ? (s[4 * i + e] * m2.x) * qs[e] : -INFINITY;
         }
-        red[(warp - 4) * 32 + lane] = reduce_scatter32<true>(s);
+        red[(warp - 8) * 32 + lane] = reduce_scatter32<true>(s);
         if (soft_any(!ok)) {
           alive = false;
           break;
@@ -816,7 +806,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
       // whole, or a part: the row began in an earlier block (slot 0) or only goes on in a later one (slot 1)
       const bool from_start = piece > 0 || first[1] == 0;
       const bool whole = from_start && w.tile + 1 == w.k.tiles;
-      red[(warp - 4) * 32 + lane] = reduce_scatter32<false>(sum_h);
+      red[(warp - 8) * 32 + lane] = reduce_scatter32<false>(sum_h);
       w.next(p);
       if (w.left > 0) {
         load_query(p, w.row, smem, qmu, t);
@@ -832,7 +822,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
       const float total_h = (rg[lane] + rg[32 + lane]) + (rg[64 + lane] + rg[96 + lane]);  // lane h: head hb + h
       float *part = p.parts + (int64_t(blockIdx.x) * 2 + (from_start ? 1 : 0)) * PX_SLOT;
       // 2^7: the tile's values are 2^-7 of the keys'; over the sum where it is whole (0 for no key; NaN stays)
-      const float inv = !whole ? 128.f : total_h > 0.f ? 128.f / total_h : total_h;
+      if (q4 == 0) oinv[hb + lane] = !whole ? 128.f : total_h > 0.f ? 128.f / total_h : total_h;
       const int dim = (key & ~7) + ((key & 7) >> 1) + 4 * (key & 1);  // of this lane's O^T row (see dequant128)
       if (q4 == 0) {
         const float m = mref[hb + lane];
@@ -844,13 +834,17 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
           part[PX_PART + H + hb + lane] = total_h;
         }
       }
+      soft_any(false);
 #pragma unroll 1
       for (int d = 0; d < 4; ++d) {
         float r[32];
         tc_ld_32x32b_x32(lanes + d * 64 + hb, reinterpret_cast<uint32_t(&)[32]>(r));
         tc_wait_ld();
 #pragma unroll
-        for (int h = 0; h < 32; ++h) r[h] *= __shfl_sync(0xffffffffu, inv, h);
+        for (int i = 0; i < 8; ++i) {
+          const float4 f = reinterpret_cast<const float4 *>(oinv + hb)[i];
+          r[4 * i] *= f.x, r[4 * i + 1] *= f.y, r[4 * i + 2] *= f.z, r[4 * i + 3] *= f.w;
+        }
         if (whole && p.o_bf16) {
           // lanes l and l ^ 2 hold neighbouring dims: of two heads the first lane stores the one, the second the other
           const bool second = lane & 2;
@@ -870,6 +864,8 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
       }
       tc_fence_before();
       soft_any(false);  // the sums and O^T have been read
+#pragma unroll
+      for (int h = 0; h < 32; ++h) sum_h[h] = 0.f;
       ++piece;
     }
     if (!alive && t == 0) report(p.err, CSA2_ERR_TIMEOUT);
@@ -883,49 +879,56 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
 }
 
 // Rows whose tiles lie in several blocks: o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over their
-// partials, in block order; and rows without a key: o = 0, lse = -inf.  One block per row and 8 heads.
+// partials, in block order; and rows without a key: o = 0, lse = -inf.  One warp per row and head; lane l holds
+// dims 4 l + 128 i ..
 __global__ void __launch_bounds__(256) prefix_combine_kernel(const __grid_constant__ PrefixArgs p) {
-  __shared__ float wts[PX_MAX_CTAS][8];
-  __shared__ float inv[8];
   grid_dep_wait();
-  const int row = blockIdx.x, h0 = 8 * blockIdx.y, t = threadIdx.x;
+  const int row = blockIdx.x, lane = threadIdx.x & 31, h = 8 * blockIdx.y + (threadIdx.x >> 5);
   const int a = p.plan[16 + row], b = p.plan[17 + row], per = p.plan[0], by_row = p.plan[1];
   // the blocks that hold a part of the row: c0 .. c0 + n - 1
   const int c0 = by_row ? row * by_row : a / per;
-  const int n = by_row ? min(by_row, b - a) : (b > a ? (b - 1) / per - c0 + 1 : 0);
+  const int n = by_row ? part_count(b - a, by_row) : (b > a ? (b - 1) / per - c0 + 1 : 0);
   if (n == 1) return;
   // the first block holds the row's start as its last piece (slot 1), the others as their first (slot 0)
   auto part = [&](int i) { return p.parts + (int64_t(c0 + i) * 2 + (i == 0 ? 1 : 0)) * PX_SLOT; };
-  if (t < 8) {
-    const int h = h0 + t;
-    float M = -INFINITY, L = 0.f;
-    for (int i = 0; i < n; ++i) M = fmaxf(M, part(i)[PX_PART + h]);
-    for (int i = 0; i < n; ++i) {
-      const float *s = part(i) + PX_PART;
-      const float w = s[h] == -INFINITY ? 0.f : ex2(s[h] - M);
-      wts[i][t] = w;
-      L += w * s[H + h];
+  float M = -INFINITY, L = 0.f;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, part(i)[PX_PART + h]);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float4 acc[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float w = 0.f, l = 0.f;  // lane i: the weight of part i0 + i, and its weighted sum
+    if (i0 + lane < n) {
+      const float *s = part(i0 + lane) + PX_PART;
+      w = s[h] == -INFINITY ? 0.f : ex2(s[h] - M);
+      l = w * s[H + h];
     }
-    inv[t] = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-    p.lse[int64_t(row) * H + h] = L == 0.f ? -INFINITY : (M - PX_BIAS + log2f(L)) * 0.69314718055994531f;
+    const int m = min(32, n - i0);
+#pragma unroll 4
+    for (int i = 0; i < m; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      L += __shfl_sync(0xffffffffu, l, i);
+      const float4 *x = reinterpret_cast<const float4 *>(part(i0 + i) + h * D) + lane;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float4 v = x[32 * u];
+        acc[u].x += wi * v.x, acc[u].y += wi * v.y, acc[u].z += wi * v.z, acc[u].w += wi * v.w;
+      }
+    }
   }
-  __syncthreads();
-  for (int it = t; it < 8 * D / 4; it += 256) {
-    const int hl = it / (D / 4), d = 4 * (it % (D / 4));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < n; ++i) {
-      const float w = wts[i][hl];
-      const float4 x = *reinterpret_cast<const float4 *>(part(i) + (h0 + hl) * D + d);
-      acc.x += w * x.x, acc.y += w * x.y, acc.z += w * x.z, acc.w += w * x.w;
-    }
-    const float s = inv[hl];
-    const int64_t at = (int64_t(row) * H + h0 + hl) * D + d;
+  const float s = L > 0.f ? 1.f / L : L;  // (0 for no key; NaN stays)
+  if (lane == 0) p.lse[int64_t(row) * H + h] = L == 0.f ? -INFINITY : (M - PX_BIAS + log2f(L)) * 0.69314718055994531f;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int64_t at = (int64_t(row) * H + h) * D + 4 * lane + 128 * u;
     if (p.o_bf16) {
-      const __nv_bfloat162 u = __floats2bfloat162_rn(acc.x * s, acc.y * s), v = __floats2bfloat162_rn(acc.z * s, acc.w * s);
+      const __nv_bfloat162 x = __floats2bfloat162_rn(acc[u].x * s, acc[u].y * s), y = __floats2bfloat162_rn(acc[u].z * s, acc[u].w * s);
       *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.o) + at) =
-          make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
+          make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
     } else {
-      *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at) = make_float4(acc.x * s, acc.y * s, acc.z * s, acc.w * s);
+      *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at) = make_float4(acc[u].x * s, acc[u].y * s, acc[u].z * s, acc[u].w * s);
     }
   }
 }
@@ -944,7 +947,7 @@ struct Layout {
   Layout(int64_t rows, int entries, int blocks) {
     shared = rows >= PX_MIN_ROWS ? entries / PX_TILE : 0;
     bad = round256(size_t(rows + 17) * 4);
-    parts = bad + round256(size_t(shared) * 4);
+    parts = bad + round256(size_t(shared) * (PX_TILE / EXPAND) * 4);
     rows16 = parts + round256(size_t(blocks) * 2 * PX_SLOT * 4);
     bytes = rows16 + size_t(shared) * PX_TILE * D * 2;
   }
@@ -976,7 +979,7 @@ void launch_prefix_attn(const uint16_t *q, int B, int Q, const int32_t *q_pos, f
   memset(&map, 0, sizeof(map));
   if (at.shared > 0 && make_half_rows_map(&map, a.rows16, int64_t(at.shared) * PX_TILE)) a.shared = at.shared;
   set_smem_limit(prefix_attn_kernel, PX_SMEM);
-  if (a.shared > 0) prefix_expand_kernel<<<a.shared, 256, 0, st>>>(a);
+  if (a.shared > 0) prefix_expand_kernel<<<a.shared * (PX_TILE / EXPAND), 256, 0, st>>>(a);
   cudaLaunchAttribute dependent[1];
   dependent[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   dependent[0].val.programmaticStreamSerializationAllowed = 1;
