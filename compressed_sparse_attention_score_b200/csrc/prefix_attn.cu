@@ -56,8 +56,8 @@ constexpr int PX_HEAD = PX_MUL + 2 * 128 * 8;     // per head: [64] logit factor
 constexpr int PX_RED = PX_HEAD + 3 * 64 * 4;      // [8 warps][32]
 constexpr int PX_QMX = PX_RED + 8 * 32 * 4;       // [8 warps][16] query maxima
 constexpr int PX_INV = PX_QMX + 8 * 16 * 4;       // [64]
-constexpr int PX_SCAN = PX_INV + 64 * 4;          // 40 ints
-constexpr int PX_BAR = PX_SCAN + 40 * 4;
+constexpr int PX_SCAN = PX_INV + 64 * 4;          // 48 ints
+constexpr int PX_BAR = PX_SCAN + 48 * 4;
 constexpr int PX_SMEM = PX_BAR + 16 * 8 + 1024;
 static_assert(PX_SMEM <= 227 * 1024, "prefix attention exceeds the shared memory of a block");
 
@@ -304,17 +304,6 @@ __device__ __forceinline__ void store_keys(const uint32_t (&h)[32], const KeyPla
           make_uint4(h[16 * i + 4 * v], h[16 * i + 4 * v + 1], h[16 * i + 4 * v + 2], h[16 * i + 4 * v + 3]);
 }
 
-// Barrier over the producer threads; returns the OR of `pred` over them.
-__device__ __forceinline__ bool prod_any(bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(uint32_t(pred))
-      : "memory");
-  return r != 0;
-}
-
 // One block of 64 dims of the prefix's tile `tile` into shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap *map, int block, int tile, uint64_t *bar) {
   asm volatile(
@@ -481,43 +470,77 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
     most = max(most, n);
     if (blockIdx.x == 0 && visible_entries(p.c, row / p.Q, p.q_pos[row]) > p.n_bound) report(p.err, CSA2_ERR_SHAPE);
   }
-  if (tid == 0) first[3] = 0;
+  // Up to 32 rows are counted by the first warp alone, which saves the block's barriers.
+  const bool few = p.rows <= 32;
   int total = 0;
-  block_exclusive_scan_1024(sum, scan, &total);
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) atomicMax(&first[3], most);
-  __syncthreads();
-  // Equal shares of all tiles in row order; or, where that makes no block's share more than an eighth longer, each row
-  // in as many equal parts as there are blocks for it.  Rows of equal length then pass over the prefix side by side, and
-  // what one of them has read is still in L2 for the others (16 rows over 65536 entries: see the file's head).
-  const int per = max(1, (total + int(gridDim.x) - 1) / int(gridDim.x)), parts = int(gridDim.x) / p.rows;
-  const bool by_row = parts > 0 && 8 * ((first[3] + parts - 1) / max(parts, 1)) <= 9 * max(per, 2);
+  if (!few) {
+    if (tid == 0) first[3] = 0;
+    block_exclusive_scan_1024(sum, scan, &total);
+    const int m = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) atomicMax(&first[3], m);
+    __syncthreads();
+    most = first[3];
+  } else if (warp == 0) {
+    total = __reduce_add_sync(0xffffffffu, sum);
+    most = __reduce_max_sync(0xffffffffu, most);
+  }
+  // Equal shares of all tiles in row order; or, where that makes no block's share more than two tiles longer (what going
+  // over to another row costs, and a little less), each row in as many equal parts as there are blocks for it.  Rows of
+  // equal length then pass over the prefix side by side, and what one of them has read is still in L2 for the others.
+  const int parts = int(gridDim.x) / p.rows;
+  int per = 0, by_row = 0, t0 = 0, t1 = 0;
+  auto share = [&]() {
+    per = max(1, (total + int(gridDim.x) - 1) / int(gridDim.x));
+    by_row = parts > 0 && (most + parts - 1) / max(parts, 1) <= per + 2 ? parts : 0;
+    t0 = blockIdx.x * per, t1 = min(total, t0 + per);
+  };
+  if (few) {
+    if (warp == 0) {
+      share();
+      int off = sum;  // lane i: the first tile of row i
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, off, o);
+        if (lane >= o) off += y;
+      }
+      off -= sum;
+      if (blockIdx.x == 0 && lane < p.rows) p.plan[16 + lane] = off;
+      int row = by_row ? int(blockIdx.x) / parts : 0;
+      if (by_row) {
+        const int n = __shfl_sync(0xffffffffu, sum, row & 31), i = blockIdx.x % parts;
+        t0 = row < p.rows ? part_start(n, i, parts) : 0, t1 = row < p.rows ? part_start(n, i + 1, parts) : 0;
+        if (lane == 0) first[0] = row, first[1] = t0;
+      } else if (sum > 0 && off <= t0 && t0 < off + sum) {
+        first[0] = lane, first[1] = t0 - off;
+      }
+      if (lane == 0) first[4] = t0, first[5] = t1;
+    }
+    __syncthreads();
+    t0 = first[4], t1 = first[5];
+  } else {
+    share();
+    if (by_row) {
+      const int row = blockIdx.x / parts, i = blockIdx.x % parts, n = row < p.rows ? row_keys(p, row).tiles : 0;
+      t0 = part_start(n, i, parts), t1 = part_start(n, i + 1, parts);
+      if (tid == 0) first[0] = row, first[1] = t0;
+    }
+    if (!by_row || blockIdx.x == 0)
+      for (int row0 = 0, base = 0; row0 < p.rows; row0 += PX_THREADS) {
+        const int row = row0 + tid;
+        const int n = row < p.rows ? row_keys(p, row).tiles : 0;
+        int all = 0;
+        const int off = base + block_exclusive_scan_1024(n, scan, &all);
+        if (blockIdx.x == 0 && row < p.rows) p.plan[16 + row] = off;
+        if (!by_row && n > 0 && off <= t0 && t0 < off + n) first[0] = row, first[1] = t0 - off;
+        base += all;
+        if (blockIdx.x != 0 && t0 < base) break;
+      }
+  }
   if (blockIdx.x == 0 && tid == 0) {
     p.plan[0] = per;
-    p.plan[1] = by_row ? parts : 0;
+    p.plan[1] = by_row;
     p.plan[16 + p.rows] = total;
   }
-  int t0 = blockIdx.x * per, t1 = min(total, t0 + per);
-  if (by_row) {
-    const int row = blockIdx.x / parts, i = blockIdx.x % parts, n = row < p.rows ? row_keys(p, row).tiles : 0;
-    t0 = part_start(n, i, parts), t1 = part_start(n, i + 1, parts);
-    if (tid == 0) first[0] = row, first[1] = t0;
-  }
-  if (t0 >= t1 && blockIdx.x != 0) return;
-  if (!by_row || blockIdx.x == 0)
-    for (int row0 = 0, base = 0; row0 < p.rows; row0 += PX_THREADS) {
-      const int row = row0 + tid;
-      const int n = row < p.rows ? row_keys(p, row).tiles : 0;
-      int all = 0;
-      const int off = base + block_exclusive_scan_1024(n, scan, &all);
-      if (blockIdx.x == 0 && row < p.rows) p.plan[16 + row] = off;
-      if (!by_row && n > 0 && off <= t0 && t0 < off + n) {
-        first[0] = row;
-        first[1] = t0 - off;
-      }
-      base += all;
-      if (blockIdx.x != 0 && t0 < base) break;
-    }
   grid_dep_launch();
   if (t0 >= t1) return;
   // entries below `limit` are read from the workspace: the shared tiles before the first bad one
@@ -533,7 +556,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   }
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 8);
       mbar_init(&freed[i], 1);
     }
     mbar_init(s_full, 1);
@@ -562,6 +585,9 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
     uint32_t h[32];
     bool ok = true;
     int seen = -1;  // the last tile whose products are known to have read it all
+    auto wait = [&](int d, int n) {
+      return __all_sync(0xffffffffu, mbar_wait_bounded(&freed[d], n & 1, abort_flag, PX_WAIT_NS));
+    };
     for (int n = 0; w.left > 0 && ok; ++n, w.next(p)) {
       if (w.within(limit)) continue;
       find_keys(p, w, at, r);
@@ -571,17 +597,14 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
         dequant_keys(at, r, h);
         if (d < 3) load_keys(p, at, d + 1, r);
         // (a barrier's parity tells only its last two phases apart: the loader's tiles in between are counted too)
-        for (; ok && seen < n - 2; ++seen) ok = mbar_wait_bounded(&freed[3], (seen + 1) & 1, abort_flag, PX_WAIT_NS);
-        if (ok && n > 0) ok = mbar_wait_bounded(&freed[d], (n - 1) & 1, abort_flag, PX_WAIT_NS);
-        if (prod_any(!ok)) {
-          ok = false;
-          break;
-        }
+        for (; ok && seen < n - 2; ++seen) ok = wait(3, seen + 1);
+        if (ok && n > 0) ok = wait(d, n - 1);
+        if (!ok) break;
         if (d == 0 && at.piece == 0) store_factors(at, r, mul + (n & 1) * 128);
         store_keys(h, at, smem + PX_K + d * 2 * 16384);
         fence_proxy_async_smem();
-        prod_any(false);
-        if (tid == 0) mbar_arrive(&full[d]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[d]);
       }
       seen = n - 1;
     }
@@ -589,7 +612,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
     regs_down<PX_REG_ISSUE>();
     if (warp == PX_LOAD_WARP) {
       // ---------------------------------------------------------- the loader of shared tiles
-      const uint32_t leader = elect_one(), kt = smem_u32(smem + PX_K);
+      const uint32_t kt = smem_u32(smem + PX_K);
       if (p.shared > 0) asm volatile("fence.proxy.async;" ::: "memory");  // (the expansion's stores were generic ones)
       bool ok = true;
       int last[4] = {-1, -1, -1, -1}, never = 0, seen = -1;
@@ -603,10 +626,12 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
         for (int d = 0; d < 4; ++d) {
           if (ok && n > 0) ok = wait(d, n - 1);
           if (ok) last[d] = n;
-          if (ok && leader) {
+          if (ok && lane == 0) {
             mbar_arrive_expect_tx(&full[d], 2 * 16384);
             tma_block(kt + (2 * d) * 16384, &map, 2 * d, w.tile, &full[d]);
             tma_block(kt + (2 * d + 1) * 16384, &map, 2 * d + 1, w.tile, &full[d]);
+          } else if (ok && lane < 8) {
+            mbar_arrive(&full[d]);  // (the barrier counts the eight producer warps)
           }
           __syncwarp();
         }
