@@ -137,6 +137,10 @@ def _stream(stream):
     return s.cuda_stream
 
 
+# The current stream of a device as a number, without the Stream object where torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _ok(status, what):
     if status != 0:
         msg = _lib.csa2_last_error_string().decode()
@@ -186,14 +190,9 @@ class GlobalKVCache:
         return (self.kv_codes, self.kv_scales, self.ix_codes, self.ix_scales)
 
     def desc(self):
-        d = csa2_cache()
-        d.kv_codes, d.kv_scales = _ptr(self.kv_codes), _ptr(self.kv_scales)
-        d.ix_codes, d.ix_scales = _ptr(self.ix_codes), _ptr(self.ix_scales)
-        d.page_table = _ptr(self.page_table)
-        d.num_entries = _ptr(self.num_entries)
-        d.num_slots, d.batch, d.ratio = self.num_slots, self.batch, self.ratio
-        d.seq_stride, d.page_size, d.max_pages = self.seq_stride, self.page_size, self.max_pages
-        return d
+        return csa2_cache(_ptr(self.kv_codes), _ptr(self.kv_scales), _ptr(self.ix_codes), _ptr(self.ix_scales),
+                          _ptr(self.page_table), _ptr(self.num_entries), self.num_slots, self.batch, self.ratio,
+                          self.seq_stride, self.page_size, self.max_pages)
 
 
 def csa2_version():
@@ -411,7 +410,7 @@ class Rotary:
             raise ValueError(f"layout must be one of {sorted(ROTARY_LAYOUT)}")
         d.step, d.rot_dim, d.first = _ptr(step), 2 * step.numel(), self.first
         d.layout, d.scale = ROTARY_LAYOUT[layout], self.scale
-        self._desc = d
+        self._desc, self._ref = d, ctypes.byref(d)
 
     @classmethod
     def table(cls, rot_dim, first=0, layout="interleaved", device="cuda", **scaling):
@@ -422,25 +421,49 @@ class Rotary:
         return self._desc
 
 
-def _rot(r):
-    return None if r is None else ctypes.byref(r.desc())
+def _rot(r, index):
+    if r is None:
+        return None
+    if r.step.get_device() != index:
+        raise ValueError("the rotary table must be on the device of the call's other tensors")
+    return r._ref
 
 
-def _on(device, stream, *tensors):
-    """The stream of a call whose tensors are all on `device` (None is no tensor), which must be the current one."""
-    if device.type != "cuda":
+def _on(t, stream):
+    """The device number of tensor t, which must be the current CUDA device, and the stream of the call."""
+    index = t.get_device()
+    if index < 0:
         raise ValueError("CSA2 tensors must live on a CUDA device")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("the tensors of a CSA2 call must be on one device")
-    if device.index != torch.cuda.current_device():
+    if index != torch.cuda.current_device():
         raise ValueError("the tensors of a CSA2 call must be on the current device")
-    return _stream(stream)
+    return index, _raw_stream(index) if stream is None else stream.cuda_stream
 
 
-def _shape(t, shape, dtype, what):
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+def _at(t, index, shape, dtype, what):
+    """The pointer of a contiguous tensor of this device, shape and type (None: NULL)."""
+    if t is None:
+        return None
+    if t.get_device() != index:
+        raise ValueError(f"{what} must be on the device of the call's other tensors")
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError("CSA2 tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _err(err, index):
+    if err is not None and (err.get_device() != index or err.dtype != torch.int32):
+        raise ValueError("err must be an int32 tensor on the device of the call's other tensors")
+    return _ptr(err)
+
+
+def _cache_on(cache, index):
+    d = cache.desc()
+    for t in (cache.kv_codes, cache.num_entries, cache.page_table):
+        if t is not None and t.get_device() != index:
+            raise ValueError("the cache must be on the device of the call's other tensors")
+    return ctypes.byref(d)
 
 
 def csa2_rotate(x, pos, rotary, inverse=False, out=None, out_dtype=None, stream=None):
@@ -449,28 +472,33 @@ def csa2_rotate(x, pos, rotary, inverse=False, out=None, out_dtype=None, stream=
     The token dims of x may be strided as long as they form one stride; out (default: a new tensor of out_dtype or
     x's type) may be x itself.  Tokens at negative positions are padding: their rows of out are left as they are.
     """
-    if x.dim() < 2 or tuple(pos.shape) != tuple(x.shape[:-2]) or pos.dtype != torch.int32:
-        raise ValueError("pos must be int32 and shaped like x without its last two dims")
+    shape = x.shape
+    if len(shape) < 2:
+        raise ValueError("x must have a heads and a dim axis")
+    index, s = _on(x, stream)
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    elif out.shape != x.shape:
-        raise ValueError("out must be shaped like x")
-    s = _on(x.device, stream, x, pos, out, rotary.step)
-    if x.dtype not in DTYPE or out.dtype not in DTYPE:
+        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
+    elif out.shape != shape or out.get_device() != index:
+        raise ValueError("out must be shaped like x, on its device")
+    xd, od = DTYPE.get(x.dtype), DTYPE.get(out.dtype)
+    if xd is None or od is None:
         raise ValueError("x and out must be float32 or bfloat16")
-    heads, dim = x.shape[-2:]
+    p = _at(pos, index, shape[:-2], torch.int32, "pos")
     (xt, xh), (ot, oh) = _head_strides(x, "x"), _head_strides(out, "out")
-    _ok(_lib.csa2_rotate(x.data_ptr(), DTYPE[x.dtype], xt, xh, out.data_ptr(), DTYPE[out.dtype], ot, oh, pos.numel(),
-                         heads, dim, _ptr(pos), _rot(rotary), int(inverse), s), "csa2_rotate")
+    _ok(_lib.csa2_rotate(x.data_ptr(), xd, xt, xh, out.data_ptr(), od, ot, oh, pos.numel(), shape[-2], shape[-1], p,
+                         _rot(rotary, index), 1 if inverse else 0, s), "csa2_rotate")
     return out
 
 
 def _head_strides(t, what):
     """(token stride, head stride) of [..., heads, dim]; the token dims must form one stride."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    shape, strides = t.shape, t.stride()
+    if shape[-1] > 1 and strides[-1] != 1:
         raise ValueError(f"{what} must have unit stride along dim")
+    if len(shape) == 3:
+        return strides[0] if shape[0] > 1 else 0, strides[1] if shape[1] > 1 else 0
     token = None
-    for n, st in reversed(list(zip(t.shape[:-2], t.stride()[:-2]))):
+    for n, st in zip(reversed(shape[:-2]), reversed(strides[:-2])):
         if n == 1:
             continue
         if token is None:
@@ -479,7 +507,7 @@ def _head_strides(t, what):
             raise ValueError(f"the token dims of {what} must form one stride")
         else:
             span = st * n
-    return token or 0, t.stride(-2) if t.shape[-2] > 1 else 0
+    return token or 0, strides[-2] if shape[-2] > 1 else 0
 
 
 def csa2_pack_kv_rotary(lat_kv, lat_ix, first_entry, cache, rot_kv, rot_ix, pool_w=None, gate_kv=None, gate_ix=None,
@@ -487,20 +515,16 @@ def csa2_pack_kv_rotary(lat_kv, lat_ix, first_entry, cache, rot_kv, rot_ix, pool
     """csa2_pack_kv / csa2_pack_kv_gated with entries turned at their positions (rot_kv / rot_ix: Rotary or None).
     kv_hat [B][T // r][512], ix_hat [B][T // r][128] bf16 (optional) receive the values that the codes stand for."""
     B, T = lat_kv.shape[0], lat_kv.shape[1]
-    _shape(lat_kv, (B, T, MAIN_DIM), lat_kv.dtype, "lat_kv")
-    _shape(lat_ix, (B, T, IX_DIM), lat_kv.dtype, "lat_ix")
-    _shape(first_entry, (B,), torch.int32, "first_entry")
-    _shape(pool_w, (B, T), torch.float32, "pool_w")
-    _shape(gate_kv, (B, T, MAIN_DIM), torch.float32, "gate_kv")
-    _shape(gate_ix, (B, T, IX_DIM), torch.float32, "gate_ix")
-    n = T // cache.ratio
-    _shape(kv_hat, (B, n, MAIN_DIM), torch.bfloat16, "kv_hat")
-    _shape(ix_hat, (B, n, IX_DIM), torch.bfloat16, "ix_hat")
-    s = _on(lat_kv.device, stream, lat_ix, first_entry, cache.kv_codes, pool_w, gate_kv, gate_ix, kv_hat, ix_hat, err)
-    d = cache.desc()
-    _ok(_lib.csa2_pack_kv_rotary(_ptr(lat_kv), _ptr(lat_ix), DTYPE[lat_kv.dtype], _ptr(pool_w), _ptr(gate_kv),
-                                 _ptr(gate_ix), B, T, _ptr(first_entry), _rot(rot_kv), _rot(rot_ix), ctypes.byref(d),
-                                 _ptr(kv_hat), _ptr(ix_hat), _ptr(err), s), "csa2_pack_kv_rotary")
+    i, s = _on(lat_kv, stream)
+    dt, f32, n = lat_kv.dtype, torch.float32, T // cache.ratio
+    _ok(_lib.csa2_pack_kv_rotary(_at(lat_kv, i, (B, T, MAIN_DIM), dt, "lat_kv"), _at(lat_ix, i, (B, T, IX_DIM), dt, "lat_ix"),
+                                 DTYPE[dt], _at(pool_w, i, (B, T), f32, "pool_w"),
+                                 _at(gate_kv, i, (B, T, MAIN_DIM), f32, "gate_kv"),
+                                 _at(gate_ix, i, (B, T, IX_DIM), f32, "gate_ix"), B, T,
+                                 _at(first_entry, i, (B,), torch.int32, "first_entry"), _rot(rot_kv, i), _rot(rot_ix, i),
+                                 _cache_on(cache, i), _at(kv_hat, i, (B, n, MAIN_DIM), torch.bfloat16, "kv_hat"),
+                                 _at(ix_hat, i, (B, n, IX_DIM), torch.bfloat16, "ix_hat"), _err(err, i), s),
+        "csa2_pack_kv_rotary")
 
 
 def csa2_append_kv_rotary(lat_kv, lat_ix, pos, cache, rot_kv, rot_ix, stage=None, kv_hat=None, ix_hat=None, err=None,
@@ -508,30 +532,28 @@ def csa2_append_kv_rotary(lat_kv, lat_ix, pos, cache, rot_kv, rot_ix, stage=None
     """csa2_append_kv of one token per sequence (lat_kv [B][512], lat_ix [B][128]) with completed entries turned at
     their positions; kv_hat [B][512], ix_hat [B][128] bf16 (optional) receive the completed entries' values."""
     B = lat_kv.shape[0]
-    _shape(lat_kv, (B, MAIN_DIM), lat_kv.dtype, "lat_kv")
-    _shape(lat_ix, (B, IX_DIM), lat_kv.dtype, "lat_ix")
-    _shape(pos, (B,), torch.int32, "pos")
-    _shape(stage, (B, cache.ratio, MAIN_DIM + IX_DIM), torch.float32, "stage")
-    _shape(kv_hat, (B, MAIN_DIM), torch.bfloat16, "kv_hat")
-    _shape(ix_hat, (B, IX_DIM), torch.bfloat16, "ix_hat")
-    s = _on(lat_kv.device, stream, lat_ix, pos, cache.kv_codes, stage, kv_hat, ix_hat, err)
-    d = cache.desc()
-    _ok(_lib.csa2_append_kv_rotary(_ptr(lat_kv), _ptr(lat_ix), DTYPE[lat_kv.dtype], B, _ptr(pos), _ptr(stage),
-                                   _rot(rot_kv), _rot(rot_ix), ctypes.byref(d), _ptr(kv_hat), _ptr(ix_hat), _ptr(err),
-                                   s), "csa2_append_kv_rotary")
+    i, s = _on(lat_kv, stream)
+    dt = lat_kv.dtype
+    _ok(_lib.csa2_append_kv_rotary(_at(lat_kv, i, (B, MAIN_DIM), dt, "lat_kv"), _at(lat_ix, i, (B, IX_DIM), dt, "lat_ix"),
+                                   DTYPE[dt], B, _at(pos, i, (B,), torch.int32, "pos"),
+                                   _at(stage, i, (B, cache.ratio, MAIN_DIM + IX_DIM), torch.float32, "stage"),
+                                   _rot(rot_kv, i), _rot(rot_ix, i), _cache_on(cache, i),
+                                   _at(kv_hat, i, (B, MAIN_DIM), torch.bfloat16, "kv_hat"),
+                                   _at(ix_hat, i, (B, IX_DIM), torch.bfloat16, "ix_hat"), _err(err, i), s),
+        "csa2_append_kv_rotary")
 
 
 def csa2_pack_swa_rotary(x, pos, swa_codes, swa_scale, rotary, err=None, stream=None):
     """csa2_pack_swa of tokens turned at their own positions (rotary: Rotary over the 512 values)."""
     B, T = x.shape[0], x.shape[1]
     R = swa_codes.shape[1]
-    _shape(x, (B, T, MAIN_DIM), x.dtype, "x")
-    _shape(pos, (B, T), torch.int32, "pos")
-    _shape(swa_codes, (B, R, MAIN_DIM), torch.uint8, "swa_codes")
-    _shape(swa_scale, (B, R), torch.float32, "swa_scale")
-    s = _on(x.device, stream, pos, swa_codes, swa_scale, rotary.step, err)
-    _ok(_lib.csa2_pack_swa_rotary(_ptr(x), DTYPE[x.dtype], B, T, _ptr(pos), _rot(rotary), _ptr(swa_codes),
-                                  _ptr(swa_scale), R, _ptr(err), s), "csa2_pack_swa_rotary")
+    i, s = _on(x, stream)
+    dt = x.dtype
+    _ok(_lib.csa2_pack_swa_rotary(_at(x, i, (B, T, MAIN_DIM), dt, "x"), DTYPE[dt], B, T,
+                                  _at(pos, i, (B, T), torch.int32, "pos"), _rot(rotary, i),
+                                  _at(swa_codes, i, (B, R, MAIN_DIM), torch.uint8, "swa_codes"),
+                                  _at(swa_scale, i, (B, R), torch.float32, "swa_scale"), R, _err(err, i), s),
+        "csa2_pack_swa_rotary")
 
 
 def csa2_prefix_workspace_size(B, Q, max_entries):
@@ -543,24 +565,21 @@ def csa2_prefix_attn(q, q_pos, cache, softmax_scale, max_entries, prefix_entries
     """Dense attention of q [B][Q][64][512] over entries whose first prefix_entries are sequence 0's for every
     sequence, joined with the SWA window if swa_codes / swa_scale are given.  Returns (o, lse)."""
     B, Q = q.shape[0], q.shape[1]
-    _shape(q, (B, Q, HEADS, MAIN_DIM), torch.bfloat16, "q")
-    _shape(q_pos, (B, Q), torch.int32, "q_pos")
+    i, s = _on(q, stream)
+    heads = (B, Q, HEADS, MAIN_DIM)
     if o is None:
-        o = torch.empty((B, Q, HEADS, MAIN_DIM), dtype=o_dtype, device=q.device)
+        o = torch.empty(heads, dtype=o_dtype, device=q.device)
     if lse is None:
         lse = torch.empty((B, Q, HEADS), dtype=torch.float32, device=q.device)
     if ws is None:
         ws = torch.empty(max(csa2_prefix_workspace_size(B, Q, max_entries), 1), dtype=torch.uint8, device=q.device)
-    _shape(o, (B, Q, HEADS, MAIN_DIM), o.dtype, "o")
-    _shape(lse, (B, Q, HEADS), torch.float32, "lse")
-    R = 0
-    if swa_codes is not None:
-        R = swa_codes.shape[1]
-        _shape(swa_codes, (B, R, MAIN_DIM), torch.uint8, "swa_codes")
-        _shape(swa_scale, (B, R), torch.float32, "swa_scale")
-    s = _on(q.device, stream, q_pos, cache.kv_codes, swa_codes, swa_scale, o, lse, ws, err)
-    d = cache.desc()
-    _ok(_lib.csa2_prefix_attn(_ptr(q), B, Q, _ptr(q_pos), softmax_scale, prefix_entries, max_entries, ctypes.byref(d),
-                              _ptr(swa_codes), _ptr(swa_scale), R, window, _ptr(o), DTYPE[o.dtype], _ptr(lse),
-                              _ptr(ws), ws.numel() * ws.element_size(), _ptr(err), s), "csa2_prefix_attn")
+    elif ws.get_device() != i:
+        raise ValueError("ws must be on the device of the call's other tensors")
+    R = 0 if swa_codes is None else swa_codes.shape[1]
+    _ok(_lib.csa2_prefix_attn(_at(q, i, heads, torch.bfloat16, "q"), B, Q, _at(q_pos, i, (B, Q), torch.int32, "q_pos"),
+                              softmax_scale, prefix_entries, max_entries, _cache_on(cache, i),
+                              _at(swa_codes, i, (B, R, MAIN_DIM), torch.uint8, "swa_codes"),
+                              _at(swa_scale, i, (B, R), torch.float32, "swa_scale"), R, window,
+                              _at(o, i, heads, o.dtype, "o"), DTYPE[o.dtype], _at(lse, i, (B, Q, HEADS), torch.float32, "lse"),
+                              _ptr(ws), ws.numel() * ws.element_size(), _err(err, i), s), "csa2_prefix_attn")
     return o, lse

@@ -2,9 +2,12 @@
 //
 // Both are HBM streaming kernels: one warp per output entry (or SWA token),
 // 16-byte vector loads, quantisation in registers, coalesced row stores.
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "kernels.cuh"
 #include "rotary.cuh"
+#include "sm100.cuh"
 
 namespace csa2 {
 
@@ -50,15 +53,44 @@ __device__ __forceinline__ void load4<uint16_t>(const uint16_t *p, float (&v)[4]
   v[2] = __uint_as_float(a.y << 16), v[3] = __uint_as_float(a.y & 0xFFFF0000u);
 }
 
-// Eight bf16 values of eight e2m1 codes (element 0 in the lowest nibble) times the scale s: at most
-// six significant bits, so exact in bf16.
-__device__ __forceinline__ uint4 hat8(uint32_t codes, float s) {
-  uint32_t w[4];
+// Two bf16 values of two e2m1 codes (one byte, low nibble first) times a scale: s16, an fp16 pair, and `after`, a power of
+// two.  At most six significant bits, so exact in fp16 and in bf16.
+__device__ __forceinline__ uint32_t hat2(uint32_t byte, uint32_t s16, float after) {
+  const uint32_t h = sm100::hmul2_u32(sm100::cvt_e2m1x2_f16x2(byte), s16);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+  return __byte_perm(__float_as_uint(f.x * after), __float_as_uint(f.y * after), 0x7632);
+}
+// Eight of them.  (For E4M3 scales the fp16 products are multiples of 2^-10 up to 2688.)
+__device__ __forceinline__ uint4 hat8(uint32_t codes, uint32_t s16, float after) {
+  return make_uint4(hat2(codes & 0xFF, s16, after), hat2((codes >> 8) & 0xFF, s16, after),
+                    hat2((codes >> 16) & 0xFF, s16, after), hat2(codes >> 24, s16, after));
+}
+
+// x / s rounded to nearest, for r = 1 / s rounded to nearest and results and remainders in normal range: an estimate corrected
+// by its exact remainder.  The corrected value is within 2^-23 ulp of the quotient before it is rounded; where s has few
+// significant bits (E4M3: four) no quotient is that close to the middle of two numbers (at least 1/30 ulp: the distance is a
+// multiple of 1 / 2 s in units of the numbers' last places), so one correction is enough.  __fdiv_rn, which takes every
+// case, is three times as long.
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  const float q = __fmul_rn(x, r);
+  return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+}
+// The same for any s: the second correction starts from an estimate within one ulp, from which q + r (x - s q) is the
+// rounded quotient (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).
+__device__ __forceinline__ float quotient_any(float x, float s, float r) {
+  const float q = quotient(x, s, r);
+  return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+}
+
+// e2m1 codes of eight values divided by s: a zero result is code 0 whatever its sign (the conversion keeps the sign).
+// The values are finite.
+__device__ __forceinline__ uint32_t codes8(const float *x, float s, float r) {
+  uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] = (__float_as_uint(e2m1_value((codes >> (8 * i)) & 15) * s) >> 16) |
-           (__float_as_uint(e2m1_value((codes >> (8 * i + 4)) & 15) * s) & 0xFFFF0000u);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+    w |= sm100::e2m1x2_code(quotient(x[2 * i], s, r), quotient(x[2 * i + 1], s, r)) << (8 * i);
+  const uint32_t m = (w | (w >> 1) | (w >> 2)) & 0x11111111u;  // nibbles with a magnitude
+  return w & (0x77777777u | (m << 3));
 }
 
 // Quantise the pooled entry a warp holds (lane l: main values [16l, 16l+16), one E4M3 block,
@@ -69,22 +101,35 @@ __device__ __forceinline__ void store_entry(const float (&x)[16], const float (&
                                             uint16_t *ix_hat = nullptr) {
   // ---- main KV: E4M3 scale per 16 values, e2m1 codes
   float amax = 0.f;
+  uint32_t bits = 0;  // the largest |bits|: values that are not finite take the general divisions
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+  for (int i = 0; i < 16; ++i) {
+    amax = fmaxf(amax, fabsf(x[i]));
+    bits = max(bits, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bits = max(bits, __float_as_uint(xi[i]) & 0x7FFFFFFFu);
   const uint32_t sc = e4m3_code(__fdiv_rn(amax, 6.0f));
   const float s = e4m3_value(sc);
   uint32_t lo = 0, hi = 0;
-  if (s != 0.f) {
+  if (__any_sync(0xffffffffu, bits >= 0x7F000000u)) {
+    if (s != 0.f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) lo |= e2m1_code(__fdiv_rn(x[i], s)) << (4 * i);
+      for (int i = 0; i < 8; ++i) lo |= e2m1_code(__fdiv_rn(x[i], s)) << (4 * i);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) hi |= e2m1_code(__fdiv_rn(x[8 + i], s)) << (4 * i);
+      for (int i = 0; i < 8; ++i) hi |= e2m1_code(__fdiv_rn(x[8 + i], s)) << (4 * i);
+    }
+  } else if (s != 0.f) {  // (a quotient below 2^-126 is code 0 whatever its last bits)
+    const float r = __frcp_rn(s);
+    lo = codes8(x, s, r);
+    hi = codes8(x + 8, s, r);
   }
   reinterpret_cast<uint2 *>(c.kv_codes + slot * CSA2_MAIN_CODE_BYTES)[lane] = make_uint2(lo, hi);
   c.kv_scales[slot * CSA2_MAIN_SCALE_BYTES + lane] = uint8_t(sc);
   if (kv_hat) {
-    reinterpret_cast<uint4 *>(kv_hat)[2 * lane] = hat8(lo, s);
-    reinterpret_cast<uint4 *>(kv_hat)[2 * lane + 1] = hat8(hi, s);
+    const uint32_t s16 = sm100::cvt_e4m3x2_f16x2(sc * 0x101u);
+    reinterpret_cast<uint4 *>(kv_hat)[2 * lane] = hat8(lo, s16, 1.f);
+    reinterpret_cast<uint4 *>(kv_hat)[2 * lane + 1] = hat8(hi, s16, 1.f);
   }
 
   // ---- indexer key: E8M0 exponent per 32 values (8 lanes), e2m1 codes
@@ -102,8 +147,8 @@ __device__ __forceinline__ void store_entry(const float (&x)[16], const float (&
   reinterpret_cast<uint16_t *>(c.ix_codes + slot * CSA2_IX_CODE_BYTES)[lane] = uint16_t(code4);
   if ((lane & 7) == 0) c.ix_scales[slot * CSA2_IX_SCALE_BYTES + (lane >> 3)] = uint8_t(ex + 127);
   if (ix_hat) {
-    const uint4 v = hat8(code4, pow2f(ex));
-    reinterpret_cast<uint2 *>(ix_hat)[lane] = make_uint2(v.x, v.y);
+    const float si = pow2f(ex);
+    reinterpret_cast<uint2 *>(ix_hat)[lane] = make_uint2(hat2(code4 & 0xFF, 0x3C003C00u, si), hat2(code4 >> 8, 0x3C003C00u, si));
   }
 }
 
@@ -188,8 +233,9 @@ __device__ __forceinline__ float exp_fixed(float x) {
 // (or fp32(1/r)), or with gate_kv / gate_ix the gated sum: per channel the softmax over the
 // entry's r tokens of the gate logits (max subtracted, exp_fixed, sum left to right, fp32
 // division) weights the tokens, summed left to right.
-// ROT: the entry is turned at its first token's position between pooling and quantisation.
-template <typename T, bool ROT>
+// ROT: the entry is turned at its first token's position between pooling and quantisation.  GATED: a kernel of its own,
+// since its registers would halve the others' occupancy.
+template <typename T, bool ROT, bool GATED>
 __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_kv,
                                                       const T *__restrict__ lat_ix,
                                                       const float *__restrict__ pool_w,
@@ -221,7 +267,7 @@ __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_
     }
   };
 
-  if (gate_kv) {
+  if constexpr (GATED) {
     // ---- gated sum: three passes over the group (max, normaliser, weighted sum)
     float m[16], mi[4], den[16], deni[4];
     for (int t = 0; t < c.ratio; ++t) {
@@ -392,7 +438,17 @@ __global__ void __launch_bounds__(256) pack_swa_kernel(const T *__restrict__ x, 
   for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const float s = __fdiv_rn(amax, 448.0f);
   uint32_t w[4] = {0, 0, 0, 0};
-  if (s != 0.f) {
+  if (s > 0x1p-60f && s < 0x1p60f) {  // (NaN values stay NaN)
+    const float r = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float2 q = make_float2(quotient_any(v[i], s, r), quotient_any(v[i + 1], s, r));
+      w[i >> 2] |= uint32_t(__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3)) << (8 * (i & 3));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // a zero result is code 0 whatever its sign
+      w[i] &= 0x7F7F7F7Fu | (((w[i] & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) & 0x80808080u);
+  } else if (s != 0.f) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i >> 2] |= e4m3_code(__fdiv_rn(v[i], s)) << (8 * (i & 3));
   }
@@ -416,9 +472,9 @@ static void pack_kv(const void *lat_kv, const void *lat_ix, const float *pool_w,
                     const RotaryWrite &rw, int32_t *err, cudaStream_t st) {
   const int64_t n = int64_t(B) * (T_ / c.ratio);
   if (n == 0) return;
-  pack_kv_kernel<T, ROT><<<unsigned((n + 7) / 8), 256, 0, st>>>(static_cast<const T *>(lat_kv),
-                                                                static_cast<const T *>(lat_ix), pool_w, gate_kv,
-                                                                gate_ix, B, T_, first_entry, c, rw, err);
+  const auto kernel = gate_kv ? pack_kv_kernel<T, ROT, true> : pack_kv_kernel<T, ROT, false>;
+  kernel<<<unsigned((n + 7) / 8), 256, 0, st>>>(static_cast<const T *>(lat_kv), static_cast<const T *>(lat_ix), pool_w,
+                                                gate_kv, gate_ix, B, T_, first_entry, c, rw, err);
 }
 
 void launch_pack_kv(const void *lat_kv, const void *lat_ix, csa2_dtype dtype, const float *pool_w,
