@@ -86,11 +86,12 @@ __device__ __forceinline__ int64_t cache_slot(const csa2_cache &c, int b, int64_
     if (n < 0 || n >= c.seq_stride) return -1;
     s = int64_t(b) * c.seq_stride + n;
   } else {
-    int64_t p = n / c.page_size;
+    const int shift = 31 - __clz(c.page_size);  // page_size is a power of two: no 64-bit divisions
+    int64_t p = n >> shift;
     if (n < 0 || p >= c.max_pages) return -1;
     int32_t pid = c.page_table[int64_t(b) * c.max_pages + p];
     if (pid < 0) return -1;
-    s = int64_t(pid) * c.page_size + (n % c.page_size);
+    s = (int64_t(pid) << shift) + (n & (c.page_size - 1));
   }
   return s < c.num_slots ? s : -1;
 }

@@ -4,6 +4,8 @@
 // 16-byte vector loads, quantisation in registers, coalesced row stores.
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.cuh"
 #include "rotary.cuh"
@@ -37,6 +39,37 @@ __device__ __forceinline__ void load16<uint16_t>(const uint16_t *p, float (&v)[1
       v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
     }
   }
+}
+
+// Sixteen values as they lie in memory, and their fp32 values.
+template <typename T>
+struct Raw16 {
+  uint4 w[sizeof(T)];  // 16 values: bf16 two words of 16 bytes, fp32 four
+  uint32_t i[sizeof(T)];  // and four more
+};
+template <typename T>
+__device__ __forceinline__ void load_raw(const T *main, const T *index, Raw16<T> &r) {
+#pragma unroll
+  for (int k = 0; k < int(sizeof(T)); ++k) r.w[k] = reinterpret_cast<const uint4 *>(main)[k];
+  if constexpr (sizeof(T) == 2) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(index);
+    r.i[0] = u.x, r.i[1] = u.y;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4 *>(index);
+    r.i[0] = u.x, r.i[1] = u.y, r.i[2] = u.z, r.i[3] = u.w;
+  }
+}
+template <typename T>
+__device__ __forceinline__ float raw_value(const uint32_t *w, int k) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w[k]);
+  return __uint_as_float((k & 1) ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
+}
+template <typename T>
+__device__ __forceinline__ void raw_values(const Raw16<T> &r, float (&v)[16], float (&vi)[4]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k] = raw_value<T>(&r.w[0].x, k);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) vi[k] = raw_value<T>(r.i, k);
 }
 
 template <typename T>
@@ -93,26 +126,39 @@ __device__ __forceinline__ uint32_t codes8(const float *x, float s, float r) {
   return w & (0x77777777u | (m << 3));
 }
 
+// max(a, |b|), NaN if either is.
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
+  return d;
+}
+
 // Quantise the pooled entry a warp holds (lane l: main values [16l, 16l+16), one E4M3 block,
 // and indexer values [4l, 4l+4), eight lanes per E8M0 block) and store it at `slot`.
 // With kv_hat / ix_hat (rows of 512 and 128 bf16) the values that the codes stand for are stored too.
 __device__ __forceinline__ void store_entry(const float (&x)[16], const float (&xi)[4], int64_t slot,
                                             const csa2_cache &c, int lane, uint16_t *kv_hat = nullptr,
                                             uint16_t *ix_hat = nullptr) {
-  // ---- main KV: E4M3 scale per 16 values, e2m1 codes
-  float amax = 0.f;
-  uint32_t bits = 0;  // the largest |bits|: values that are not finite take the general divisions
+  float amax = 0.f, am = 0.f;  // (NaN if a value is)
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    amax = fmaxf(amax, fabsf(x[i]));
-    bits = max(bits, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  for (int i = 0; i < 16; ++i) amax = max_abs_nan(amax, x[i]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) am = max_abs_nan(am, xi[i]);
+  // values that are not finite, or nearly not, take the general divisions
+  const bool special = __any_sync(0xffffffffu, !(amax < 0x1p126f) || !(am < 0x1p126f));
+  if (special) {
+    amax = am = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) am = fmaxf(am, fabsf(xi[i]));
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) bits = max(bits, __float_as_uint(xi[i]) & 0x7FFFFFFFu);
+
+  // ---- main KV: E4M3 scale per 16 values, e2m1 codes
   const uint32_t sc = e4m3_code(__fdiv_rn(amax, 6.0f));
   const float s = e4m3_value(sc);
   uint32_t lo = 0, hi = 0;
-  if (__any_sync(0xffffffffu, bits >= 0x7F000000u)) {
+  if (special) {
     if (s != 0.f) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) lo |= e2m1_code(__fdiv_rn(x[i], s)) << (4 * i);
@@ -133,16 +179,21 @@ __device__ __forceinline__ void store_entry(const float (&x)[16], const float (&
   }
 
   // ---- indexer key: E8M0 exponent per 32 values (8 lanes), e2m1 codes
-  float am = fmaxf(fmaxf(fabsf(xi[0]), fabsf(xi[1])), fmaxf(fabsf(xi[2]), fabsf(xi[3])));
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
   uint32_t code4 = 0;
   int ex = -127;
   if (am != 0.f) {
     ex = e8m0_ceil_exponent(__fdiv_rn(am, 6.0f));
-    const float si = pow2f(ex);
+    if (special) {
+      const float si = pow2f(ex);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) code4 |= e2m1_code(__fdiv_rn(xi[i], si)) << (4 * i);
+      for (int i = 0; i < 4; ++i) code4 |= e2m1_code(__fdiv_rn(xi[i], si)) << (4 * i);
+    } else {
+      const float by = pow2f(-ex);  // (a power of two: the product is the quotient)
+      code4 = sm100::e2m1x2_code(xi[0] * by, xi[1] * by) | sm100::e2m1x2_code(xi[2] * by, xi[3] * by) << 8;
+      code4 &= 0x7777u | ((code4 | (code4 >> 1) | (code4 >> 2)) & 0x1111u) << 3;
+    }
   }
   reinterpret_cast<uint16_t *>(c.ix_codes + slot * CSA2_IX_CODE_BYTES)[lane] = uint16_t(code4);
   if ((lane & 7) == 0) c.ix_scales[slot * CSA2_IX_SCALE_BYTES + (lane >> 3)] = uint8_t(ex + 127);
@@ -171,43 +222,65 @@ __device__ __forceinline__ void turn_pair(float &a, float &b, double2 cs, float 
   b = float((x * cs.y + y * cs.x) * g);
 }
 
-// Turn the values a warp holds (x: main, lane l 16l ..; xi: indexer, lane l 4l .., or none) at
-// position pos: through the warp's row `buf` of shared memory, one pair per lane and step.
-template <bool IX>
-__device__ __forceinline__ void turn_values(float (&x)[16], float (&xi)[4], const csa2_rotary &kv, const csa2_rotary &ix,
-                                            bool same, int64_t pos, float *buf, int lane) {
+// Turn the values a warp holds (x: main, lane l 16l ..; xi: indexer, lane l 4l .., or none) through the warp's row `buf` of
+// shared memory: turn_pairs(kv or ix, its part of the row) turns the pairs in place there.
+template <bool IX, typename F>
+__device__ __forceinline__ void turn_through(float (&x)[16], float (&xi)[4], bool main, bool index, float *buf, int lane,
+                                             F &&turn_pairs) {
   __syncwarp();  // the row's previous use is over
-  if (kv.rot_dim) {
+  if (main) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<float4 *>(buf + turn_at(16 * lane) + 4 * i) =
           make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
   }
-  if (IX && ix.rot_dim) *reinterpret_cast<float4 *>(buf + TURN_MAIN + 4 * lane) = make_float4(xi[0], xi[1], xi[2], xi[3]);
+  if (IX && index) *reinterpret_cast<float4 *>(buf + TURN_MAIN + 4 * lane) = make_float4(xi[0], xi[1], xi[2], xi[3]);
   __syncwarp();
-  for (int i = lane; i < kv.rot_dim / 2; i += 32) {
-    const double2 cs = rotary_cs64(kv.step[i], pos);
-    turn_pair(buf[turn_at(rotary_dim0(kv, i))], buf[turn_at(rotary_dim1(kv, i))], cs, kv.scale);
-    if (IX && same)
-      turn_pair(buf[TURN_MAIN + rotary_dim0(ix, i)], buf[TURN_MAIN + rotary_dim1(ix, i)], cs, ix.scale);
-  }
-  if (IX && !same)
-    for (int i = lane; i < ix.rot_dim / 2; i += 32)
-      turn_pair(buf[TURN_MAIN + rotary_dim0(ix, i)], buf[TURN_MAIN + rotary_dim1(ix, i)],
-                rotary_cs64(ix.step[i], pos), ix.scale);
+  turn_pairs();
   __syncwarp();
-  if (kv.rot_dim) {
+  if (main) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 v = *reinterpret_cast<const float4 *>(buf + turn_at(16 * lane) + 4 * i);
       x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
     }
   }
-  if (IX && ix.rot_dim) {
+  if (IX && index) {
     const float4 v = *reinterpret_cast<const float4 *>(buf + TURN_MAIN + 4 * lane);
     xi[0] = v.x, xi[1] = v.y, xi[2] = v.z, xi[3] = v.w;
   }
 }
+__device__ __forceinline__ void turn_main(const csa2_rotary &kv, int i, double2 cs, float *buf) {
+  turn_pair(buf[turn_at(rotary_dim0(kv, i))], buf[turn_at(rotary_dim1(kv, i))], cs, kv.scale);
+}
+__device__ __forceinline__ void turn_index(const csa2_rotary &ix, int i, double2 cs, float *buf) {
+  turn_pair(buf[TURN_MAIN + rotary_dim0(ix, i)], buf[TURN_MAIN + rotary_dim1(ix, i)], cs, ix.scale);
+}
+
+// At position pos, one pair per lane and step.
+template <bool IX>
+__device__ __forceinline__ void turn_values(float (&x)[16], float (&xi)[4], const csa2_rotary &kv, const csa2_rotary &ix,
+                                            bool same, int64_t pos, float *buf, int lane) {
+  turn_through<IX>(x, xi, kv.rot_dim != 0, ix.rot_dim != 0, buf, lane, [&]() {
+    for (int i = lane; i < kv.rot_dim / 2; i += 32) {
+      const double2 cs = rotary_cs64(kv.step[i], pos);
+      turn_main(kv, i, cs, buf);
+      if (IX && same) turn_index(ix, i, cs, buf);
+    }
+    if (IX && !same)
+      for (int i = lane; i < ix.rot_dim / 2; i += 32) turn_index(ix, i, rotary_cs64(ix.step[i], pos), buf);
+  });
+}
+
+// cos and sin of a pair at a position that goes up in equal steps: each is the last one turned by a step's angle (an error of
+// 2^-53 a step; a new start after at most 16).
+struct Turning {
+  double2 at, by;
+  __device__ __forceinline__ void start(uint64_t step, int64_t pos) { at = rotary_cs64(step, pos); }
+  __device__ __forceinline__ void next() {
+    at = make_double2(at.x * by.x - at.y * by.y, at.x * by.y + at.y * by.x);
+  }
+};
 
 // exp(x) from a fixed sequence of fp32 operations (so that the gated compressor's weights,
 // and through them the quantised codes, do not depend on a math library): t = x log2(e),
@@ -329,6 +402,80 @@ __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_
   }
 
   finish();
+}
+
+// The rotating pack of a chunk whose main and indexer values share one table of at most 32 pairs: a warp takes `run`
+// consecutive entries (lanes as in pack_kv_kernel; lane l turns pair l), so that a sine and cosine in fp64 serve a run, and asks
+// for the next entry's first token before it quantises this one.
+template <typename T>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3)
+    pack_run_kernel(const T *__restrict__ lat_kv, const T *__restrict__ lat_ix, const float *__restrict__ pool_w, int T_,
+                    int n_new, int64_t all, int run, const int32_t *__restrict__ first_entry, csa2_cache c, RotaryWrite rw,
+                    int32_t *err) {
+  __shared__ float turn_buf[8][TURN_ROW];
+  const int lane = threadIdx.x & 31, r = c.ratio;
+  float *buf = turn_buf[threadIdx.x >> 5];
+  int64_t e = (int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5)) * run;
+  int left = int(min(int64_t(run), all - e));
+  if (left <= 0) return;
+  int b = int(e / n_new), j = int(e % n_new);
+  Turning turning;
+  const bool turns = lane < max(rw.kv.rot_dim, rw.ix.rot_dim) / 2;
+  const uint64_t step = turns ? (rw.kv.rot_dim ? rw.kv.step : rw.ix.step)[lane] : 0;
+  turning.by = rotary_cs64(step, r);
+  const bool one = r == 1 && !pool_w;  // the entry is its token
+  const float w_default = __fdiv_rn(1.0f, float(r));
+  Raw16<T> raw;
+  auto load = [&](int64_t tok) { load_raw(lat_kv + tok * D + 16 * lane, lat_ix + tok * DI + 4 * lane, raw); };
+  load(int64_t(b) * T_ + int64_t(j) * r);
+  int64_t first = first_entry[b];
+  bool fresh = true;
+  for (; left > 0; --left, ++e) {
+    const int64_t n = first + j, slot = cache_slot(c, b, n);
+    float x[16], xi[4];
+    raw_values(raw, x, xi);
+    if (!one) {
+      const int64_t tok0 = int64_t(b) * T_ + int64_t(j) * r;
+      const float w0 = pool_w ? pool_w[tok0] : w_default;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(w0, x[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xi[i] = __fmul_rn(w0, xi[i]);
+      for (int t = 1; t < r; ++t) {
+        const float wt = pool_w ? pool_w[tok0 + t] : w_default;
+        load(tok0 + t);
+        float v[16], vi[4];
+        raw_values(raw, v, vi);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = __fadd_rn(x[i], __fmul_rn(wt, v[i]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xi[i] = __fadd_rn(xi[i], __fmul_rn(wt, vi[i]));
+      }
+    }
+    // this entry's angle; then on to the next one
+    if (fresh) turning.start(step, n * r);
+    else turning.next();
+    fresh = false;
+    if (++j == n_new) {
+      j = 0, ++b;
+      fresh = true;
+    }
+    if (left > 1) {
+      load(int64_t(b) * T_ + int64_t(j) * r);
+      if (fresh) first = first_entry[b];
+    }
+    turn_through<true>(x, xi, rw.kv.rot_dim != 0, rw.ix.rot_dim != 0, buf, lane, [&]() {
+      if (turns) {
+        if (rw.kv.rot_dim) turn_main(rw.kv, lane, turning.at, buf);
+        if (rw.ix.rot_dim) turn_index(rw.ix, lane, turning.at, buf);
+      }
+    });
+    if (slot < 0) {
+      if (lane == 0) report(err, CSA2_ERR_INDEX);
+    } else {
+      store_entry(x, xi, slot, c, lane, rw.kv_hat ? rw.kv_hat + e * D : nullptr, rw.ix_hat ? rw.ix_hat + e * DI : nullptr);
+    }
+  }
 }
 
 // Decode-time append, one warp per sequence (lanes as in pack_kv_kernel).  The token at
@@ -472,6 +619,13 @@ static void pack_kv(const void *lat_kv, const void *lat_ix, const float *pool_w,
                     const RotaryWrite &rw, int32_t *err, cudaStream_t st) {
   const int64_t n = int64_t(B) * (T_ / c.ratio);
   if (n == 0) return;
+  if (ROT && !gate_kv && (rw.same || !rw.kv.rot_dim || !rw.ix.rot_dim) && rw.kv.rot_dim <= 64 && rw.ix.rot_dim <= 64) {
+    // runs of up to 16 entries, as long as every SM still gets 16 warps
+    const int run = int(std::min<int64_t>(16, std::max<int64_t>(1, n / (int64_t(sm_count()) * 16))));
+    pack_run_kernel<T><<<unsigned((n + 8 * run - 1) / (8 * run)), 256, 0, st>>>(
+        static_cast<const T *>(lat_kv), static_cast<const T *>(lat_ix), pool_w, T_, T_ / c.ratio, n, run, first_entry, c, rw, err);
+    return;
+  }
   const auto kernel = gate_kv ? pack_kv_kernel<T, ROT, true> : pack_kv_kernel<T, ROT, false>;
   kernel<<<unsigned((n + 7) / 8), 256, 0, st>>>(static_cast<const T *>(lat_kv), static_cast<const T *>(lat_ix), pool_w,
                                                 gate_kv, gate_ix, B, T_, first_entry, c, rw, err);
