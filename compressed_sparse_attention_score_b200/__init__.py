@@ -16,7 +16,8 @@ _NAMES = ("EXPORTED", "MODE", "GlobalKVCache", "csa2_cache", "csa2_check", "csa2
 def __getattr__(name):
     if name in _NAMES:
         from . import _lib
-        return getattr(_lib, name)
+        value = globals()[name] = getattr(_lib, name)  # (found without this function from now on)
+        return value
     raise AttributeError(name)
 
 

@@ -52,11 +52,15 @@ constexpr int PX_K = 0;                           // key tile: 8 x 16 KB
 constexpr int PX_Q = PX_K + 8 * 16384;            // query heads in fp16: 8 chunks of 64 dims x 64 heads
 constexpr int PX_P = PX_Q + 8 * 8192;             // P^T: 128 keys x 64 heads fp16
 constexpr int PX_MUL = PX_P + 16384;              // [2][128] logit and weight multipliers of the tile's keys
-constexpr int PX_HEAD = PX_MUL + 2 * 128 * 8;     // per head: [64] logit factors, references, negated references
-constexpr int PX_RED = PX_HEAD + 3 * 64 * 4;      // [8 warps][32]
-constexpr int PX_QMX = PX_RED + 8 * 32 * 4;       // [8 warps][16] query maxima
-constexpr int PX_INV = PX_QMX + 8 * 16 * 4;       // [64]
-constexpr int PX_SCAN = PX_INV + 64 * 4;          // 48 ints
+constexpr int PX_QMU = PX_MUL + 2 * 128 * 8;      // [64] logit factor of each head
+// What each lane quarter's softmax warps keep for themselves, [4][64] each: the references m, BIAS - m, and the factors of a
+// finished row.
+constexpr int PX_MREF = PX_QMU + 64 * 4;
+constexpr int PX_NREF = PX_MREF + 4 * 64 * 4;
+constexpr int PX_INV = PX_NREF + 4 * 64 * 4;
+constexpr int PX_RED = PX_INV + 4 * 64 * 4;       // [8 warps][32] maxima
+constexpr int PX_SUM = PX_RED + 8 * 32 * 4;       // [8 warps][32] sums
+constexpr int PX_SCAN = PX_SUM + 8 * 32 * 4;      // 48 ints
 constexpr int PX_BAR = PX_SCAN + 48 * 4;
 constexpr int PX_SMEM = PX_BAR + 16 * 8 + 1024;
 static_assert(PX_SMEM <= 227 * 1024, "prefix attention exceeds the shared memory of a block");
@@ -359,13 +363,18 @@ __device__ __forceinline__ uint32_t elect_one() {
   return r;
 }
 
-// Four heads' logit factors and negated references (nref stands 2 H floats behind qmu).  Volatile: kept where they
-// are used, or all heads' would take the registers at once.
-__device__ __forceinline__ void lds_pair(float4 &q, float4 &r, uint32_t at) {
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%8];\n\tld.shared.v4.f32 {%4, %5, %6, %7}, [%8 + %9];"
+// Four heads' logit factors and negated references.  Volatile: kept where they are used, or all heads' would take the
+// registers at once.
+__device__ __forceinline__ void lds_pair(float4 &q, float4 &r, uint32_t q_at, uint32_t r_at) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%8];\n\tld.shared.v4.f32 {%4, %5, %6, %7}, [%9];"
                : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w), "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
-               : "r"(at), "n"(2 * H * 4)
+               : "r"(q_at), "r"(r_at)
                : "memory");
+}
+__device__ __forceinline__ float redux_max(float x) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -402,46 +411,42 @@ __device__ __forceinline__ void tc_st_32x32b_x32(uint32_t taddr, const uint32_t 
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // The query heads of `row` in fp16, scaled per head by a power of two (query_prescale_exp), into the Q
-// operand; qmu[h] = 2^7 tau log2(e) 2^-s (the tile holds 2^-7 of the keys).  Called by the softmax threads (t of 256); contains two barriers of
-// theirs, the first before anything is written.
-__device__ __forceinline__ void load_query(const PrefixArgs &p, int row, uint8_t *smem, float *qmu, int t) {
-  uint32_t *qmx = reinterpret_cast<uint32_t *>(smem + PX_QMX);
-  const uint4 *src = reinterpret_cast<const uint4 *>(p.q + int64_t(row) * H * D);
-  const int warp = t >> 5, pair = warp & ~1;  // the two warps that hold the heads t / 64 + 4 u
-  uint4 v[16];  // chunk t + 256 u: head t / 64 + 4 u, dims 8 (t % 64) ..
+// operand; qmu[h] = 2^7 tau log2(e) 2^-s (the tile holds 2^-7 of the keys).  A softmax warp takes the heads 8 w ..; nothing
+// waits: every warp has read the previous row's factors, and the tensor core its query, when one gets here.
+__device__ __forceinline__ void load_query(const PrefixArgs &p, int row, uint8_t *smem, float *qmu, int w, int lane) {
+  const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (int64_t(row) * H + 8 * w) * D) + lane;
+  uint4 v[16];  // head 8 w + u / 2, dims 8 lane + 256 (u % 2) ..
 #pragma unroll
-  for (int u = 0; u < 16; ++u) v[u] = src[t + 256 * u];
+  for (int u = 0; u < 16; ++u) v[u] = src[32 * u];
 #pragma unroll
-  for (int u = 0; u < 16; ++u) {
-    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+  for (int hh = 0; hh < 8; ++hh) {
     uint32_t mb = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mb = max(mb, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-    mb = __reduce_max_sync(0xffffffffu, mb);
-    if ((t & 31) == 0) qmx[warp * 16 + u] = mb;
-  }
-  soft_any(false);
+    for (int u = 2 * hh; u < 2 * hh + 2; ++u) {
+      const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
-  for (int u = 0; u < 16; ++u) {
-    const float sc = pow2f(query_prescale_exp(max(qmx[pair * 16 + u], qmx[pair * 16 + 16 + u])));
-    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-    uint32_t o4[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // dims i and i + 4 of the eight
-      const uint32_t lo = w[i >> 1], hi = w[2 + (i >> 1)];
-      const __half2 hv = __floats2half2_rn(__uint_as_float((i & 1) ? lo & 0xFFFF0000u : lo << 16) * sc,
-                                           __uint_as_float((i & 1) ? hi & 0xFFFF0000u : hi << 16) * sc);
-      o4[i] = *reinterpret_cast<const uint32_t *>(&hv);
+      for (int i = 0; i < 4; ++i) mb = max(mb, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
     }
-    const int h = (t >> 6) + 4 * u, u8 = t & 63;
-    *reinterpret_cast<uint4 *>(smem + PX_Q + (u8 / 8) * 8192 + kmaj128(h, u8 % 8)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-  }
-  if (t < H) {
-    const int c = t & 3, u = t >> 2;
-    qmu[t] = 128.f * p.tau2 * pow2f(-query_prescale_exp(max(qmx[2 * c * 16 + u], qmx[(2 * c + 1) * 16 + u])));
+    const int e = query_prescale_exp(__reduce_max_sync(0xffffffffu, mb)), h = 8 * w + hh;
+    const float sc = pow2f(e);
+#pragma unroll
+    for (int u = 2 * hh; u < 2 * hh + 2; ++u) {
+      const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      uint32_t o4[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // dims i and i + 4 of the eight
+        const uint32_t lo = x[i >> 1], hi = x[2 + (i >> 1)];
+        const __half2 hv = __floats2half2_rn(__uint_as_float((i & 1) ? lo & 0xFFFF0000u : lo << 16) * sc,
+                                             __uint_as_float((i & 1) ? hi & 0xFFFF0000u : hi << 16) * sc);
+        o4[i] = *reinterpret_cast<const uint32_t *>(&hv);
+      }
+      const int u8 = lane + 32 * (u & 1);
+      *reinterpret_cast<uint4 *>(smem + PX_Q + (u8 / 8) * 8192 + kmaj128(h, u8 % 8)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+    }
+    if (lane == 0) qmu[h] = 128.f * p.tau2 * pow2f(-e);
   }
   fence_proxy_async_smem();
-  soft_any(false);
+  __syncwarp();
 }
 
 __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid_constant__ CUtensorMap map,
@@ -449,10 +454,8 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float2 *mul = reinterpret_cast<float2 *>(smem + PX_MUL);
-  float *qmu = reinterpret_cast<float *>(smem + PX_HEAD);  // logit factor of each head
-  float *mref = qmu + H, *nref = mref + H;                 // reference m, and BIAS - m
-  float *red = reinterpret_cast<float *>(smem + PX_RED);
-  float *oinv = reinterpret_cast<float *>(smem + PX_INV);  // [64] what a finished row is multiplied by
+  float *qmu = reinterpret_cast<float *>(smem + PX_QMU);
+  float *red = reinterpret_cast<float *>(smem + PX_RED), *sums = reinterpret_cast<float *>(smem + PX_SUM);
   int *scan = reinterpret_cast<int *>(smem + PX_SCAN);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + PX_BAR);  // [4] pair of blocks written
   uint64_t *freed = full + 4;                                    // [4] pair of blocks consumed
@@ -562,7 +565,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
     mbar_init(s_full, 1);
     mbar_init(o_full, 1);
     mbar_init(p_full, 1);
-    mbar_init(q_full, 1);
+    mbar_init(q_full, 8);
     mbar_init(idle, 1);
     *abort_flag = 0;
     mbar_init_fence();
@@ -704,14 +707,17 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
     // ------------------------------------------------------------ softmax
     regs_up<PX_REG_SOFT>();
     const int t = tid - PX_PROD, q4 = warp & 3, hb = 32 * ((warp - 8) >> 2), key = 32 * q4 + lane;
-    const uint32_t lanes = tmem + (uint32_t(32 * q4) << 16), head = smem_u32(qmu + hb);
+    const uint32_t lanes = tmem + (uint32_t(32 * q4) << 16);
+    float *mref = reinterpret_cast<float *>(smem + PX_MREF) + 64 * q4 + hb, *nref = reinterpret_cast<float *>(smem + PX_NREF) + 64 * q4 + hb;
+    float *oinv = reinterpret_cast<float *>(smem + PX_INV) + 64 * q4 + hb;
+    const uint32_t q_at = smem_u32(qmu + hb), r_at = smem_u32(nref);
     float sum_h[32];
 #pragma unroll
     for (int h = 0; h < 32; ++h) sum_h[h] = 0.f;
     int piece = 0;
     bool begins = true, alive = true;
-    load_query(p, w.row, smem, qmu, t);
-    if (t == 0) mbar_arrive(q_full);
+    load_query(p, w.row, smem, qmu, warp - 8, lane);
+    if (lane == 0) mbar_arrive(q_full);
     for (int n = 0; w.left > 0; ++n) {
       const bool ok = mbar_wait_bounded(s_full, n & 1, abort_flag, PX_WAIT_NS);
       tc_fence_after();
@@ -732,7 +738,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
 #pragma unroll
           for (int i = 4 * g; i < 4 * g + 4; ++i) {
             float4 q, r;
-            lds_pair(q, r, head + 16 * i);
+            lds_pair(q, r, q_at + 16 * i, r_at + 16 * i);
             float x[4] = {s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]};
             if (!plain) {
 #pragma unroll
@@ -770,34 +776,38 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
       // P^T is written before it is known whether a reference has to move; it seldom has, except where a piece
       // begins.  (Once moved the references are the maxima so far: there is no third round.)
       for (int round = begins ? 0 : 1;; ++round) {
-        const float top = round == 0 ? INFINITY : weights();
-        if (!soft_any(!ok || (round < 2 && top > PX_LAG + PX_BIAS))) break;
+        if (round > 0) {
+          const float top = weights();
+          if (!soft_any(!ok || (round == 1 && top > PX_LAG + PX_BIAS))) break;
+        }
         // new references; O^T and the sums follow (O^T holds nothing yet where a piece begins)
         tc_ld_32x32b_x32(lanes + PX_TMEM_S + hb, reinterpret_cast<uint32_t(&)[32]>(s));
         tc_wait_ld();
+        float most = -INFINITY;  // lane h: the warp's maximum of head hb + h
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float4 q, r;
-          lds_pair(q, r, head + 16 * i);
+          lds_pair(q, r, q_at + 16 * i, r_at + 16 * i);
           const float qs[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[4 * i + e] = valid ? (s[4 * i + e] * m2.x) * qs[e] : -INFINITY;
+          for (int e = 0; e < 4; ++e) {
+            const float m = redux_max(valid ? (s[4 * i + e] * m2.x) * qs[e] : -INFINITY);
+            if (lane == 4 * i + e) most = m;
+          }
         }
-        red[(warp - 8) * 32 + lane] = reduce_scatter32<true>(s);
+        red[(warp - 8) * 32 + lane] = most;
         if (soft_any(!ok)) {
           alive = false;
           break;
         }
         const float *rg = red + (hb >> 5) * 128;
-        const float most = fmaxf(fmaxf(rg[lane], rg[32 + lane]), fmaxf(rg[64 + lane], rg[96 + lane]));
-        const float old = round == 0 ? -INFINITY : mref[hb + lane];
+        most = fmaxf(fmaxf(rg[lane], rg[32 + lane]), fmaxf(rg[64 + lane], rg[96 + lane]));
+        const float old = round == 0 ? -INFINITY : mref[lane];
         const float now = fmaxf(old, most);
         const float alpha = old == -INFINITY ? 0.f : ex2(old - now);  // lane h: head hb + h
-        soft_any(false);  // every warp has read the old references and the maxima
-        if (q4 == 0) {
-          mref[hb + lane] = now;
-          nref[hb + lane] = PX_BIAS - now;
-        }
+        mref[lane] = now;  // (every quarter's warps find the same)
+        nref[lane] = PX_BIAS - now;
+        __syncwarp();
         if (round > 0) {
 #pragma unroll
           for (int h = 0; h < 32; ++h) sum_h[h] *= __shfl_sync(0xffffffffu, alpha, h);
@@ -813,7 +823,6 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
           tc_wait_st();
           tc_fence_before();
         }
-        soft_any(false);  // the new references are written
         round = 1;
       }
       if (!alive) break;
@@ -831,11 +840,11 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
       // whole, or a part: the row began in an earlier block (slot 0) or only goes on in a later one (slot 1)
       const bool from_start = piece > 0 || first[1] == 0;
       const bool whole = from_start && w.tile + 1 == w.k.tiles;
-      red[(warp - 8) * 32 + lane] = reduce_scatter32<false>(sum_h);
+      sums[(warp - 8) * 32 + lane] = reduce_scatter32<false>(sum_h);
       w.next(p);
       if (w.left > 0) {
-        load_query(p, w.row, smem, qmu, t);
-        if (t == 0) mbar_arrive(q_full);
+        load_query(p, w.row, smem, qmu, warp - 8, lane);
+        if (lane == 0) mbar_arrive(q_full);
       }
       const bool o_ok = mbar_wait_bounded(o_full, piece & 1, abort_flag, PX_WAIT_NS);
       tc_fence_after();
@@ -843,14 +852,15 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
         alive = false;
         break;
       }
-      const float *rg = red + (hb >> 5) * 128;
-      const float total_h = (rg[lane] + rg[32 + lane]) + (rg[64 + lane] + rg[96 + lane]);  // lane h: head hb + h
+      const float *sg = sums + (hb >> 5) * 128;
+      const float total_h = (sg[lane] + sg[32 + lane]) + (sg[64 + lane] + sg[96 + lane]);  // lane h: head hb + h
       float *part = p.parts + (int64_t(blockIdx.x) * 2 + (from_start ? 1 : 0)) * PX_SLOT;
       // 2^7: the tile's values are 2^-7 of the keys'; over the sum where it is whole (0 for no key; NaN stays)
-      if (q4 == 0) oinv[hb + lane] = !whole ? 128.f : total_h > 0.f ? 128.f / total_h : total_h;
-      const int dim = (key & ~7) + ((key & 7) >> 1) + 4 * (key & 1);  // of this lane's O^T row (see dequant128)
+      oinv[lane] = !whole ? 128.f : total_h > 0.f ? 128.f / total_h : total_h;
+      __syncwarp();
+      const int dim = (key & ~7) + ((key & 7) >> 1) + 4 * (key & 1);  // of this lane's O^T row (see unpack8)
       if (q4 == 0) {
-        const float m = mref[hb + lane];
+        const float m = mref[lane];
         if (whole) {
           p.lse[int64_t(row) * H + hb + lane] =
               total_h == 0.f ? -INFINITY : (m - PX_BIAS + log2f(total_h)) * 0.69314718055994531f;
@@ -859,7 +869,6 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
           part[PX_PART + H + hb + lane] = total_h;
         }
       }
-      soft_any(false);
 #pragma unroll 1
       for (int d = 0; d < 4; ++d) {
         float r[32];
@@ -867,7 +876,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
         tc_wait_ld();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float4 f = reinterpret_cast<const float4 *>(oinv + hb)[i];
+          const float4 f = reinterpret_cast<const float4 *>(oinv)[i];
           r[4 * i] *= f.x, r[4 * i + 1] *= f.y, r[4 * i + 2] *= f.z, r[4 * i + 3] *= f.w;
         }
         if (whole && p.o_bf16) {
@@ -887,8 +896,8 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
           for (int h = 0; h < 32; ++h) orow[h * D] = r[h];
         }
       }
+      // (the next products into O^T, and the next sums, stand behind the softmax threads' next barrier)
       tc_fence_before();
-      soft_any(false);  // the sums and O^T have been read
 #pragma unroll
       for (int h = 0; h < 32; ++h) sum_h[h] = 0.f;
       ++piece;
