@@ -167,7 +167,8 @@ __device__ __forceinline__ uint32_t scale128(uint32_t byte) { return hmul2_u32(c
 // written an entry.
 constexpr int EXPAND = 32;
 __global__ void __launch_bounds__(256) prefix_expand_kernel(const __grid_constant__ PrefixArgs p) {
-  grid_dep_launch();
+  grid_dep_wait();    // (the table and the planes may be the previous kernel's work)
+  grid_dep_launch();  // from here on the attention kernel may start, and read what was written before this call
   const int lane = threadIdx.x & 31, j0 = blockIdx.x * EXPAND + 4 * (threadIdx.x >> 5);
   int32_t page[4];
   uint32_t slot[4], sc[4];
@@ -464,6 +465,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   volatile int *abort_flag = reinterpret_cast<volatile int *>(s_full + 6);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
+  if (p.shared == 0) grid_dep_wait();  // (the inputs may be the previous kernel's work)
   // ---- the plan: the tiles of all rows and of the longest, and this block's share
   int *first = scan + 36;  // this block's first row, first tile of it, shared tiles, longest row
   int sum = 0, most = 0;
@@ -859,6 +861,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
       oinv[lane] = !whole ? 128.f : total_h > 0.f ? 128.f / total_h : total_h;
       __syncwarp();
       const int dim = (key & ~7) + ((key & 7) >> 1) + 4 * (key & 1);  // of this lane's O^T row (see unpack8)
+      float ahead[16];
       if (q4 == 0) {
         const float m = mref[lane];
         if (whole) {
@@ -870,30 +873,34 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
         }
       }
 #pragma unroll 1
-      for (int d = 0; d < 4; ++d) {
-        float r[32];
-        tc_ld_32x32b_x32(lanes + d * 64 + hb, reinterpret_cast<uint32_t(&)[32]>(r));
+      for (int g = 0; g < 8; ++g) {  // 128 dims of 16 heads at a time, the next ones on their way
+        const int d = g >> 1, h0 = 16 * (g & 1);
+        float r[16];
+        if (g == 0) tc_ld_32x32b_x16(lanes + hb, reinterpret_cast<uint32_t(&)[16]>(ahead));
         tc_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 f = reinterpret_cast<const float4 *>(oinv)[i];
-          r[4 * i] *= f.x, r[4 * i + 1] *= f.y, r[4 * i + 2] *= f.z, r[4 * i + 3] *= f.w;
+        for (int i = 0; i < 4; ++i) {
+          const float4 f = reinterpret_cast<const float4 *>(oinv + h0)[i];
+          r[4 * i] = ahead[4 * i] * f.x, r[4 * i + 1] = ahead[4 * i + 1] * f.y;
+          r[4 * i + 2] = ahead[4 * i + 2] * f.z, r[4 * i + 3] = ahead[4 * i + 3] * f.w;
         }
+        if (g < 7)
+          tc_ld_32x32b_x16(lanes + ((g + 1) >> 1) * 64 + 16 * ((g + 1) & 1) + hb, reinterpret_cast<uint32_t(&)[16]>(ahead));
         if (whole && p.o_bf16) {
           // lanes l and l ^ 2 hold neighbouring dims: of two heads the first lane stores the one, the second the other
           const bool second = lane & 2;
           uint32_t *orow = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.o) +
-                                                        (int64_t(row) * H + hb + (second ? 1 : 0)) * D + 128 * d + (dim & ~1));
+                                                        (int64_t(row) * H + hb + h0 + (second ? 1 : 0)) * D + 128 * d + (dim & ~1));
 #pragma unroll
-          for (int h = 0; h < 32; h += 2) {
+          for (int h = 0; h < 16; h += 2) {
             const float got = __shfl_xor_sync(0xffffffffu, second ? r[h] : r[h + 1], 2);
             const __nv_bfloat162 v = second ? __floats2bfloat162_rn(got, r[h + 1]) : __floats2bfloat162_rn(r[h], got);
             orow[h * (D / 2)] = *reinterpret_cast<const uint32_t *>(&v);
           }
         } else {
-          float *orow = (whole ? static_cast<float *>(p.o) + (int64_t(row) * H + hb) * D : part + hb * D) + 128 * d + dim;
+          float *orow = (whole ? static_cast<float *>(p.o) + (int64_t(row) * H + hb + h0) * D : part + (hb + h0) * D) + 128 * d + dim;
 #pragma unroll
-          for (int h = 0; h < 32; ++h) orow[h * D] = r[h];
+          for (int h = 0; h < 16; ++h) orow[h * D] = r[h];
         }
       }
       // (the next products into O^T, and the next sums, stand behind the softmax threads' next barrier)
@@ -1013,22 +1020,26 @@ void launch_prefix_attn(const uint16_t *q, int B, int Q, const int32_t *q_pos, f
   memset(&map, 0, sizeof(map));
   if (at.shared > 0 && make_half_rows_map(&map, a.rows16, int64_t(at.shared) * PX_TILE)) a.shared = at.shared;
   set_smem_limit(prefix_attn_kernel, PX_SMEM);
-  if (a.shared > 0) prefix_expand_kernel<<<a.shared * (PX_TILE / EXPAND), 256, 0, st>>>(a);
+  // Every kernel may be launched while the one before it ends: each waits for it before it reads or writes anything.
   cudaLaunchAttribute dependent[1];
   dependent[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   dependent[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
+  cfg.attrs = dependent;
+  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(256);
+  if (a.shared > 0) {
+    cfg.gridDim = dim3(a.shared * (PX_TILE / EXPAND));
+    cudaLaunchKernelEx(&cfg, prefix_expand_kernel, a);
+  }
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(PX_THREADS);
   cfg.dynamicSmemBytes = PX_SMEM;
-  cfg.stream = st;
-  cfg.attrs = dependent;
-  cfg.numAttrs = a.shared > 0 ? 1 : 0;  // only behind a kernel of this call
   cudaLaunchKernelEx(&cfg, prefix_attn_kernel, map, a);
   cfg.gridDim = dim3(rows, H / 8);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  cfg.numAttrs = 1;
   cudaLaunchKernelEx(&cfg, prefix_combine_kernel, a);
 }
 
