@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   uint64_t *freed = full + 4;                                    // [4] pair of blocks consumed
   uint64_t *s_full = freed + 4, *o_full = s_full + 1, *p_full = s_full + 2, *q_full = s_full + 3, *idle = s_full + 4;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 5);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(s_full + 6);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(s_full + 6), *moving = abort_flag + 1;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (p.shared == 0) grid_dep_wait();  // (the inputs may be the previous kernel's work)
@@ -566,10 +566,11 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
     }
     mbar_init(s_full, 1);
     mbar_init(o_full, 1);
-    mbar_init(p_full, 1);
+    mbar_init(p_full, 8);
     mbar_init(q_full, 8);
     mbar_init(idle, 1);
     *abort_flag = 0;
+    *moving = 0;
     mbar_init_fence();
   }
   tc_fence_before();
@@ -678,14 +679,21 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
         commit_to(leader, &freed[d]);
       };
       bool begins = true, more = true;
-      for (int n = 0, piece = 0; more; ++n) {
+      for (int n = 0, piece = 0, written = 0; more; ++n) {
         if (begins) {  // S^T of a piece's first tile
           if (!wait(q_full, piece)) break;
           if (!step_s(n, 0, true) || !step_s(n, 1, false) || !step_s(n, 2, false) || !step_s(n, 3, false)) break;
           commit_to(leader, s_full);
         }
         const bool ends = w.ends_piece();
-        if (!wait(p_full, n)) break;
+        // P^T counts once all warps have written it, unless one of them has found that a reference has to move: then once
+        // they have all written it again
+        if (!wait(p_full, written++)) break;
+        if (*moving) {
+          if (!wait(p_full, written++)) break;
+          *moving = 0;
+          __syncwarp();
+        }
 #pragma unroll
         for (int d = 0; d < 4; ++d) step_o(d, begins);
         if (ends) {
@@ -780,7 +788,12 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
       for (int round = begins ? 0 : 1;; ++round) {
         if (round > 0) {
           const float top = weights();
-          if (!soft_any(!ok || (round == 1 && top > PX_LAG + PX_BIAS))) break;
+          const bool moves = __any_sync(0xffffffffu, round == 1 && top > PX_LAG + PX_BIAS);
+          if (lane == 0) {  // (the vote below is off the tensor core's path)
+            if (moves) *moving = 1;
+            mbar_arrive(p_full);
+          }
+          if (!soft_any(!ok || moves)) break;
         }
         // new references; O^T and the sums follow (O^T holds nothing yet where a piece begins)
         tc_ld_32x32b_x32(lanes + PX_TMEM_S + hb, reinterpret_cast<uint32_t(&)[32]>(s));
@@ -828,7 +841,6 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
         round = 1;
       }
       if (!alive) break;
-      if (t == 0) mbar_arrive(p_full);
       const bool ends = w.ends_piece();
 #pragma unroll
       for (int h = 0; h < 32; h += 2) add2(sum_h[h], sum_h[h + 1], s[h], s[h + 1]);
