@@ -327,7 +327,6 @@ __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_
     if (lane == 0) report(err, CSA2_ERR_INDEX);
     return;
   }
-  const float w_default = __fdiv_rn(1.0f, float(c.ratio));
   float x[16], xi[4];
   const int64_t tok0 = int64_t(b) * T_ + int64_t(j) * c.ratio;
   auto finish = [&]() {
@@ -384,23 +383,20 @@ __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_
         xi[i] = t == 0 ? term : __fadd_rn(xi[i], term);
       }
     }
-    finish();
-    return;
-  }
-
-  // ---- pool the tokens of this entry (fp32, left to right, no fused multiply-add)
-  for (int t = 0; t < c.ratio; ++t) {
-    const int64_t tok = int64_t(b) * T_ + int64_t(j) * c.ratio + t;
-    const float wt = pool_w ? pool_w[tok] : w_default;
-    float v[16], vi[4];
-    load16<T>(lat_kv + tok * D + 16 * lane, v);
-    load4<T>(lat_ix + tok * DI + 4 * lane, vi);
+  } else {
+    // ---- pool the tokens of this entry (fp32, left to right, no fused multiply-add)
+    const float w_default = __fdiv_rn(1.0f, float(c.ratio));
+    for (int t = 0; t < c.ratio; ++t) {
+      const float wt = pool_w ? pool_w[tok0 + t] : w_default;
+      float v[16], vi[4];
+      load16<T>(lat_kv + (tok0 + t) * D + 16 * lane, v);
+      load4<T>(lat_ix + (tok0 + t) * DI + 4 * lane, vi);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = t == 0 ? __fmul_rn(wt, v[i]) : __fadd_rn(x[i], __fmul_rn(wt, v[i]));
+      for (int i = 0; i < 16; ++i) x[i] = t == 0 ? __fmul_rn(wt, v[i]) : __fadd_rn(x[i], __fmul_rn(wt, v[i]));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) xi[i] = t == 0 ? __fmul_rn(wt, vi[i]) : __fadd_rn(xi[i], __fmul_rn(wt, vi[i]));
+      for (int i = 0; i < 4; ++i) xi[i] = t == 0 ? __fmul_rn(wt, vi[i]) : __fadd_rn(xi[i], __fmul_rn(wt, vi[i]));
+    }
   }
-
   finish();
 }
 

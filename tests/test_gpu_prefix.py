@@ -307,3 +307,144 @@ def test_decode_steps_with_rotation(layout):
             assert np.abs(to_np(o[b, 0]) - wo).max() <= 1e-2
             turned = R.turn(to_np(o[b, 0]).astype(np.float64), np.full(64, p), *arg, inverse=True)
             np.testing.assert_allclose(to_np(back[b]), turned, rtol=2.0 ** -8, atol=1e-5)
+
+
+# ------------------------------------------------------------------ the prefix dequantised ahead (many rows or a long prefix)
+def everything(t, values=None):
+    """Plain float64 attention of every query of the batch on the GPU: o [B][Q][64][512], lse."""
+    o = torch.zeros((t.B, t.Q, 64, 512), dtype=torch.float64, device=DEV)
+    lse = torch.full((t.B, t.Q, 64), -float("inf"), dtype=torch.float64, device=DEV)
+    pre = torch.from_numpy(t.prefix).to(DEV)
+    for b in range(t.B):
+        own = torch.from_numpy(t.values[b]).to(DEV)
+        count = int(t.cache.num_entries[b])
+        for i in range(t.Q):
+            p = int(t.q_pos[b, i])
+            if p < 0:
+                continue
+            keys = torch.cat((pre, own))[:min(count, (p + 1) // t.ratio)]
+            if t.gone is not None:
+                keys = keys[~t.gone[b, :len(keys)]]
+            if t.window:
+                at = torch.arange(max(0, p - t.window + 1), p + 1, device=DEV) % t.ring
+                codes = t.codes[b, at].view(torch.float8_e4m3fn).double()
+                keys = torch.cat((keys, codes * t.scale[b, at].double()[:, None]))
+            if len(keys):
+                x = t.q[b, i].double() @ keys.T * TAU
+                lse[b, i] = torch.logsumexp(x, -1)
+                o[b, i] = torch.softmax(x, -1) @ keys
+    return o, lse
+
+
+Batch.gone = None
+AHEAD = [  # S, tails, ratio, page, window, Q: at least 4 rows and 400 row-tiles of the prefix
+    (10500, [5, 0, 260, 128, 33], 4, 256, 128, 1), (12800, [0, 1, 127, 300], 1, 16, 0, 1),
+    (140, [11 * (b % 5) for b in range(70)], 1, 16, 128, 6), (1300, [7 * (b % 9) for b in range(45)], 2, 64, 0, 1),
+    (400, [b % 4 for b in range(40)], 1, 0, 100, 4), (129, [200 * (b % 2) for b in range(410)], 4, 64, 0, 1)]
+
+
+@pytest.mark.parametrize("S,tails,ratio,page,window,Q", AHEAD)
+def test_prefix_dequantised_ahead(S, tails, ratio, page, window, Q):
+    t = Batch(S, tails, ratio, page, window, Q, seed=21)
+    assert t.B * Q >= 4 and t.B * Q * (S // 128) >= 400
+    t.cache.num_entries[1] = min(int(t.cache.num_entries[1]), S // 2)  # one row sees half of the prefix
+    if t.B > 4:
+        t.q_pos[4] = -1                                                 # and one nothing
+    ws = torch.full((K().csa2_prefix_workspace_size(t.B, Q, t.most),), 0xFF, dtype=torch.uint8, device=DEV)
+    wo, wl = everything(t)
+    for od in (torch.float32, torch.bfloat16):
+        o, lse = t.run(o_dtype=od, ws=ws)
+        assert K().csa2_check(t.err) == 0
+        check(o, lse, (to_np(wo), to_np(wl)), f"{od}")
+    o2, lse2 = t.run(o_dtype=torch.bfloat16, ws=ws)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_pages_outside_the_cache_in_a_prefix_dequantised_ahead():
+    """Pages of the prefix that lie outside the cache: reported, their entries left out of every row, whether before,
+    between or behind the good ones."""
+    for pages in ((0,), (100, 101, 333), (656,)):
+        t = Batch(10500, [5, 0, 260, 128, 33], 4, 16, 128, 1, seed=22)
+        t.gone = torch.zeros((5, 10500 + 300), dtype=torch.bool, device=DEV)
+        for n, page in enumerate(pages):
+            t.cache.page_table[0, page] = (-1, 1 << 20, -7)[n]
+            t.gone[:, 16 * page:min(16 * page + 16, 10500)] = True
+            t.gone[0, 16 * page:16 * page + 16] = True  # (the prefix's last page holds sequence 0's first own entries)
+        o, lse = t.run()
+        assert K().csa2_check(t.err) == 5
+        check(o, lse, tuple(to_np(x) for x in everything(t)), f"pages {pages}")
+
+
+def test_short_bound_with_a_prefix_dequantised_ahead():
+    """max_entries below the prefix: reported, and only that many entries count."""
+    k = K()
+    t = Batch(12900, [0, 1, 127, 300], 1, 16, 128, 1, seed=23)
+    o, lse = k.csa2_prefix_attn(t.q, t.q_pos, t.cache, TAU, 12801, 12900, swa_codes=t.codes, swa_scale=t.scale, err=t.err)
+    assert k.csa2_check(t.err) == 2
+    t.cache.num_entries.clamp_(max=12801)
+    check(o, lse, tuple(to_np(x) for x in everything(t)), "bounded")
+
+
+@pytest.mark.parametrize("S,B", [(300, 3), (12800, 4)])
+def test_heads_that_are_not_finite_stay_alone(S, B):
+    """Infinities and NaN in some query heads: every other head is as without them."""
+    t = Batch(S, [3] * B, 1, 16, 128, 1, seed=24)
+    wo, wl = everything(t)
+    t.q[0, 0, 7, 100], t.q[1, 0, 0, 0], t.q[2, 0, 63, 511] = float("inf"), float("nan"), -float("inf")
+    o, lse = t.run()
+    assert K().csa2_check(t.err) == 0
+    keep = torch.ones((B, 1, 64), dtype=torch.bool, device=DEV)
+    keep[0, 0, 7] = keep[1, 0, 0] = keep[2, 0, 63] = False
+    check(o[keep], lse[keep], (to_np(wo[keep]), to_np(wl[keep])), "the other heads")
+
+
+def test_two_calls_at_once_and_a_captured_one():
+    """Two streams with a workspace each, over one cache; then the long call captured and replayed on other queries."""
+    t = Batch(12800, [0, 1, 127, 300], 1, 16, 128, 1, seed=25)
+    u = Batch(12800, [0, 1, 127, 300], 1, 16, 128, 1, seed=25)
+    u.q.copy_(make(u.q.shape, 77, torch.bfloat16))
+    want = [tuple(to_np(x) for x in everything(x)) for x in (t, u)]
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x, s, got in zip((t, u), streams, outs):
+            with torch.cuda.stream(s):
+                got.append(x.run())
+    torch.cuda.synchronize()
+    for got, w in zip(outs, want):
+        for o, lse in got:
+            check(o, lse, w, "two streams")
+    ws = torch.empty(K().csa2_prefix_workspace_size(t.B, 1, t.most), dtype=torch.uint8, device=DEV)
+    o, lse = torch.zeros_like(outs[0][0][0]), torch.zeros_like(outs[0][0][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        t.run(ws=ws, o=o, lse=lse)
+        t.run(ws=ws, o=o, lse=lse)  # (one after the other in one workspace)
+    t.q.copy_(u.q)
+    for _ in range(2):
+        ws.fill_(0xFF)
+        graph.replay()
+    torch.cuda.synchronize()
+    check(o, lse, tuple(to_np(x) for x in everything(t)), "replayed")
+
+
+def test_very_large_and_very_small_logits():
+    """Softmax scales that spread the logits over millions, and that leave them all but equal; keys of one repeated value
+    (every weight the same, whatever the reference)."""
+    k = K()
+    for S, B in ((700, 2), (12800, 4)):
+        t = Batch(S, [3] * B, 1, 16, 0, 1, seed=26)
+        for tau in (1e-6, 3.0, 1e5):
+            o, lse = k.csa2_prefix_attn(t.q, t.q_pos, t.cache, tau, t.most, t.S, err=t.err)
+            x = torch.einsum("bqhd,nd->bqhn", t.q.double(), torch.from_numpy(t.prefix).to(DEV))
+            own = torch.stack([torch.einsum("qhd,nd->qhn", t.q[b].double(), torch.from_numpy(t.values[b]).to(DEV)) for b in range(B)])
+            x = torch.cat((x, own), -1) * float(np.float32(tau))
+            wl = torch.logsumexp(x, -1)
+            assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+            # logits are fp32: off by a few 2^-24 of their size
+            size = x.abs().amax(-1)
+            assert bool(((lse.double() - wl).abs() <= 1e-4 + size * 2.0 ** -21).all())
+            if tau <= 3.0:
+                vals = [torch.cat((torch.from_numpy(t.prefix).to(DEV), torch.from_numpy(t.values[b]).to(DEV))) for b in range(B)]
+                wo = torch.stack([torch.softmax(x[b], -1) @ vals[b] for b in range(B)])
+                check(o, lse, (to_np(wo), to_np(lse.double())), f"tau {tau}")
