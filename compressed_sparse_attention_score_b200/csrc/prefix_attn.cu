@@ -166,38 +166,37 @@ __device__ __forceinline__ void unpack8(uint32_t w, uint32_t s128, uint32_t *o) 
 // 2^7 times an E4M3 scale, in both halves (at most 57344).
 __device__ __forceinline__ uint32_t scale128(uint32_t byte) { return hmul2_u32(cvt_e4m3x2_f16x2(byte * 0x101u), 0x58005800u); }
 
-// The prefix's complete tiles in fp16, 32 entries a block, four a warp.  Memory bound: 288 bytes read and 1 KB
-// written an entry.
+// The prefix's complete tiles in fp16, 32 entries a block, four a warp; lane l holds dims 8 l .. and 256 + 8 l .., so that every
+// load and store of a warp is one contiguous piece.  Memory bound: 288 bytes read and 1 KB written an entry.
 constexpr int EXPAND = 32;
 __global__ void __launch_bounds__(256) prefix_expand_kernel(const __grid_constant__ PrefixArgs p) {
   grid_dep_wait();    // (the table and the planes may be the previous kernel's work)
   grid_dep_launch();  // from here on the attention kernel may start, and read what was written before this call
   const int lane = threadIdx.x & 31, j0 = blockIdx.x * EXPAND + 4 * (threadIdx.x >> 5);
   int32_t page[4];
-  uint32_t slot[4], sc[4];
-  uint2 codes[4];
+  uint32_t slot[4], sc[4][2], codes[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i) page[i] = entry_page(p, 0, j0 + i);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     slot[i] = entry_slot(p, 0, j0 + i, page[i]);
-    codes[i] = make_uint2(0u, 0u);
-    sc[i] = 0u;
-    if (slot[i] != NO_SLOT) {
-      codes[i] = reinterpret_cast<const uint2 *>(p.c.kv_codes + int64_t(slot[i]) * CSA2_MAIN_CODE_BYTES)[lane];
-      sc[i] = p.c.kv_scales[int64_t(slot[i]) * CSA2_MAIN_SCALE_BYTES + lane];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      codes[i][u] = sc[i][u] = 0u;
+      if (slot[i] != NO_SLOT) {
+        codes[i][u] = reinterpret_cast<const uint32_t *>(p.c.kv_codes + int64_t(slot[i]) * CSA2_MAIN_CODE_BYTES)[32 * u + lane];
+        sc[i][u] = p.c.kv_scales[int64_t(slot[i]) * CSA2_MAIN_SCALE_BYTES + 16 * u + (lane >> 1)];
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t h[8];
-    const uint32_t s = scale128(sc[i]);
-    unpack8(codes[i].x, s, h);
-    unpack8(codes[i].y, s, h + 4);
-    uint4 *o = reinterpret_cast<uint4 *>(p.rows16 + int64_t(j0 + i) * D) + 2 * lane;
-    o[0] = make_uint4(h[0], h[1], h[2], h[3]);
-    o[1] = make_uint4(h[4], h[5], h[6], h[7]);
-  }
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t h[4];
+      unpack8(codes[i][u], scale128(sc[i][u]), h);
+      reinterpret_cast<uint4 *>(p.rows16 + int64_t(j0 + i) * D)[32 * u + lane] = make_uint4(h[0], h[1], h[2], h[3]);
+    }
   const int any = __syncthreads_or(slot[0] == NO_SLOT || slot[1] == NO_SLOT || slot[2] == NO_SLOT || slot[3] == NO_SLOT);
   if (threadIdx.x == 0) p.bad[blockIdx.x] = any;
 }
