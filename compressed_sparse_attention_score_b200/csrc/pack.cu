@@ -94,9 +94,20 @@ __device__ __forceinline__ uint32_t hat2(uint32_t byte, uint32_t s16, float afte
   return __byte_perm(__float_as_uint(f.x * after), __float_as_uint(f.y * after), 0x7632);
 }
 // Eight of them.  (For E4M3 scales the fp16 products are multiples of 2^-10 up to 2688.)
-__device__ __forceinline__ uint4 hat8(uint32_t codes, uint32_t s16, float after) {
-  return make_uint4(hat2(codes & 0xFF, s16, after), hat2((codes >> 8) & 0xFF, s16, after),
-                    hat2((codes >> 16) & 0xFF, s16, after), hat2(codes >> 24, s16, after));
+__device__ __forceinline__ uint4 hat8(uint32_t codes, uint32_t s16) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(codes));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = sm100::hmul2_u32(h[i], s16);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    h[i] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+  }
+  return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
 // x / s rounded to nearest, for r = 1 / s rounded to nearest and results and remainders in normal range: an estimate corrected
@@ -118,10 +129,16 @@ __device__ __forceinline__ float quotient_any(float x, float s, float r) {
 // e2m1 codes of eight values divided by s: a zero result is code 0 whatever its sign (the conversion keeps the sign).
 // The values are finite.
 __device__ __forceinline__ uint32_t codes8(const float *x, float s, float r) {
-  uint32_t w = 0;
+  float q[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w |= sm100::e2m1x2_code(quotient(x[2 * i], s, r), quotient(x[2 * i + 1], s, r)) << (8 * i);
+  for (int i = 0; i < 8; ++i) q[i] = quotient(x[i], s, r);
+  uint32_t w;  // (the conversion puts its first operand in the high nibble)
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
   const uint32_t m = (w | (w >> 1) | (w >> 2)) & 0x11111111u;  // nibbles with a magnitude
   return w & (0x77777777u | (m << 3));
 }
@@ -174,8 +191,8 @@ __device__ __forceinline__ void store_entry(const float (&x)[16], const float (&
   c.kv_scales[slot * CSA2_MAIN_SCALE_BYTES + lane] = uint8_t(sc);
   if (kv_hat) {
     const uint32_t s16 = sm100::cvt_e4m3x2_f16x2(sc * 0x101u);
-    reinterpret_cast<uint4 *>(kv_hat)[2 * lane] = hat8(lo, s16, 1.f);
-    reinterpret_cast<uint4 *>(kv_hat)[2 * lane + 1] = hat8(hi, s16, 1.f);
+    reinterpret_cast<uint4 *>(kv_hat)[2 * lane] = hat8(lo, s16);
+    reinterpret_cast<uint4 *>(kv_hat)[2 * lane + 1] = hat8(hi, s16);
   }
 
   // ---- indexer key: E8M0 exponent per 32 values (8 lanes), e2m1 codes
