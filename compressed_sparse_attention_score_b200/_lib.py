@@ -443,13 +443,13 @@ def _at(t, index, shape, dtype, what):
     """The pointer of a contiguous tensor of this device, shape and type (None: NULL)."""
     if t is None:
         return None
+    if t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
     if t.get_device() != index:
         raise ValueError(f"{what} must be on the device of the call's other tensors")
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError("CSA2 tensors must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{what} must be contiguous")
 
 
 def _err(err, index):

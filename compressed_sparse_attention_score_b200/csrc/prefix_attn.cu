@@ -550,6 +550,8 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   }
   grid_dep_launch();
   if (t0 >= t1) return;
+  if (tid < 512)  // the first query row on its way into L2 while the block is set up
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + int64_t(first[0]) * H * D + 64 * tid));
   // entries below `limit` are read from the workspace: the shared tiles before the first bad one
   int *limit_at = first + 2;
   if (tid == 0) *limit_at = p.shared;
@@ -946,32 +948,47 @@ __global__ void __launch_bounds__(256) prefix_combine_kernel(const __grid_consta
   if (n == 1) return;
   // the first block holds the row's start as its last piece (slot 1), the others as their first (slot 0)
   auto part = [&](int i) { return p.parts + (int64_t(c0 + i) * 2 + (i == 0 ? 1 : 0)) * PX_SLOT; };
-  float M = -INFINITY, L = 0.f;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, part(i)[PX_PART + h]);
+  // the statistics of the first 32 parts, and the values of the first four, asked for together
+  float m = -INFINITY, l = 0.f;
+  if (lane < n) m = part(lane)[PX_PART + h], l = part(lane)[PX_PART + H + h];
+  float4 x[4][4];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i0 + i < n) {
+        const float4 *src = reinterpret_cast<const float4 *>(part(i0 + i) + h * D) + lane;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[i][u] = src[32 * u];
+      }
+  };
+  load(0);
+  float M = m, L = 0.f;
+  for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, part(i)[PX_PART + h]);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float4 acc[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float w = 0.f, l = 0.f;  // lane i: the weight of part i0 + i, and its weighted sum
-    if (i0 + lane < n) {
-      const float *s = part(i0 + lane) + PX_PART;
-      w = s[h] == -INFINITY ? 0.f : ex2(s[h] - M);
-      l = w * s[H + h];
-    }
-    const int m = min(32, n - i0);
-#pragma unroll 4
-    for (int i = 0; i < m; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      L += __shfl_sync(0xffffffffu, l, i);
-      const float4 *x = reinterpret_cast<const float4 *>(part(i0 + i) + h * D) + lane;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float4 v = x[32 * u];
-        acc[u].x += wi * v.x, acc[u].y += wi * v.y, acc[u].z += wi * v.z, acc[u].w += wi * v.w;
+  float w = 0.f;  // lane i: the weight of part i0 + i, and (l) its weighted sum
+  for (int i0 = 0; i0 < n; i0 += 4) {
+    if ((i0 & 31) == 0) {
+      if (i0 > 0) {
+        m = -INFINITY, l = 0.f;
+        if (i0 + lane < n) m = part(i0 + lane)[PX_PART + h], l = part(i0 + lane)[PX_PART + H + h];
       }
+      w = m == -INFINITY ? 0.f : ex2(m - M);
+      l = w == 0.f ? 0.f : w * l;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i0 + i >= n) break;
+      const float wi = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
+      L += __shfl_sync(0xffffffffu, l, (i0 + i) & 31);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        acc[u].x += wi * x[i][u].x, acc[u].y += wi * x[i][u].y, acc[u].z += wi * x[i][u].z, acc[u].w += wi * x[i][u].w;
+    }
+    if (i0 + 4 < n) load(i0 + 4);
   }
   const float s = L > 0.f ? 1.f / L : L;  // (0 for no key; NaN stays)
   if (lane == 0) p.lse[int64_t(row) * H + h] = L == 0.f ? -INFINITY : (M - PX_BIAS + log2f(L)) * 0.69314718055994531f;
