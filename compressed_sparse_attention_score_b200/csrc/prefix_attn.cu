@@ -160,12 +160,14 @@ __device__ __forceinline__ uint32_t entry_slot(const PrefixArgs &p, int b, int j
 
 // Eight 4-bit codes times 2^-7 s (s128: 2^7 s in both halves) in fp16: o[e] holds elements e and e + 4, the order that a
 // word unpacks to pairwise (the query and the output use the same order of dims).  A code's three magnitude bits,
-// moved to bits 9 - 11 of an fp16 number, are 2^-14 of its value (subnormal for 0.5, as in e2m1).
+// moved to bits 9 - 11 of an fp16 number, are 2^-14 of its value (subnormal for 0.5, as in e2m1): four codes at a time to
+// the high bytes of such numbers, then a byte permutation each.
 __device__ __forceinline__ void unpack8(uint32_t w, uint32_t s128, uint32_t *o) {
-  o[0] = hmul2_u32(((w << 12) & 0x80008000u) | ((w << 9) & 0x0E000E00u), s128);
-  o[1] = hmul2_u32(((w << 8) & 0x80008000u) | ((w << 5) & 0x0E000E00u), s128);
-  o[2] = hmul2_u32(((w << 4) & 0x80008000u) | ((w << 1) & 0x0E000E00u), s128);
-  o[3] = hmul2_u32((w & 0x80008000u) | ((w >> 3) & 0x0E000E00u), s128);
+  const uint32_t even = ((w << 4) & 0x80808080u) | ((w << 1) & 0x0E0E0E0Eu), odd = (w & 0x80808080u) | ((w >> 3) & 0x0E0E0E0Eu);
+  o[0] = hmul2_u32(__byte_perm(even, 0u, 0x2404), s128);
+  o[1] = hmul2_u32(__byte_perm(odd, 0u, 0x2404), s128);
+  o[2] = hmul2_u32(__byte_perm(even, 0u, 0x3414), s128);
+  o[3] = hmul2_u32(__byte_perm(odd, 0u, 0x3414), s128);
 }
 // 2^7 times an E4M3 scale, in both halves (at most 57344).
 __device__ __forceinline__ uint32_t scale128(uint32_t byte) { return hmul2_u32(cvt_e4m3x2_f16x2(byte * 0x101u), 0x58005800u); }
