@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   for (int row = tid; row < p.rows; row += PX_THREADS) {
     const RowKeys k = row_keys(p, row);
     const int n = k.tiles;
-    copied_tiles = min(p.shared, k.nks / PX_TILE);
+    copied_tiles = min(p.shared, k.nks / PX_TILE);  // (read for up to 32 rows, a lane's own)
     sum += n;
     most = max(most, n);
     if (blockIdx.x == 0 && visible_entries(p.c, row / p.Q, p.q_pos[row]) > p.n_bound) report(p.err, CSA2_ERR_SHAPE);
@@ -561,7 +561,11 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
     p.plan[16 + p.rows] = total;
   }
   grid_dep_launch();
-  if (t0 >= t1) return;
+  if (t0 >= t1) {
+    grid_dep_wait();  // (so that this kernel's end implies the expansion's)
+    return;
+  }
+  if (!few) __syncthreads();  // first[0] and [1] are written
   if (tid < 512)  // the first query row on its way into L2 while the block is set up
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + int64_t(first[0]) * H * D + 64 * tid));
   // entries below `limit` are read from the workspace: the shared tiles before the first bad one
