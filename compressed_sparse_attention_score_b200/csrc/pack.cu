@@ -419,7 +419,9 @@ __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_
 
 // The rotating pack of a chunk whose main and indexer values share one table of at most 32 pairs: a warp takes `run`
 // consecutive entries (lanes as in pack_kv_kernel; lane l turns pair l), so that a sine and cosine in fp64 serve a run, and asks
-// for the next entry's first token before it quantises this one.
+// for the next entry's first token before it quantises this one.  Bound by instruction issue (about 570 a warp and
+// entry): 131288 bf16 tokens, r = 1, with the values stored, 100 us (58 % of the copy rate; a sine and cosine per
+// entry 162 us).
 template <typename T>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3)
     pack_run_kernel(const T *__restrict__ lat_kv, const T *__restrict__ lat_ix, const float *__restrict__ pool_w, int T_,

@@ -22,6 +22,13 @@
 // The reference m_h moves only when a logit exceeds it by 2^LAG, so O^T is rarely rescaled; weights are held
 // as 2^(x - m + BIAS), which keeps weights down to 2^-29 of the largest in fp16 while 2^(LAG + BIAS) stays far
 // below its maximum.  The sums are fp32 of the unrounded weights.
+//
+// What bounds it: a product of 128 x 64 x 16 reads 6 KB of shared memory (48.8 clocks; the tensor core would take 32), a
+// tile has 64 of them, and its 128 KB are written there too: 4150 clocks a tile, 4850 measured (2.75 us; 4.9 us where the
+// tile is dequantised in the block).  The rest is the softmax between a tile's products; TMEM and shared memory
+// hold one row's tile, so nothing else can run meanwhile.
+// Measured (whole call): 32 rows over 8192 shared entries 73 us, 96 over 4096 100 us, 16 over 65536 216 us (641
+// TFLOP/s), 13 over 2999 36 us, 2 over 96 23 us.
 #include <cuda_fp16.h>
 #include <string.h>
 
@@ -173,7 +180,8 @@ __device__ __forceinline__ void unpack8(uint32_t w, uint32_t s128, uint32_t *o) 
 __device__ __forceinline__ uint32_t scale128(uint32_t byte) { return hmul2_u32(cvt_e4m3x2_f16x2(byte * 0x101u), 0x58005800u); }
 
 // The prefix's complete tiles in fp16, 32 entries a block, four a warp; lane l holds dims 8 l .. and 256 + 8 l .., so that every
-// load and store of a warp is one contiguous piece.  Memory bound: 288 bytes read and 1 KB written an entry.
+// load and store of a warp is one contiguous piece.  Memory bound: 288 bytes read and 1 KB written an entry
+// (65536 entries: 15 us).
 constexpr int EXPAND = 32;
 __global__ void __launch_bounds__(256) prefix_expand_kernel(const __grid_constant__ PrefixArgs p) {
   grid_dep_wait();    // (the table and the planes may be the previous kernel's work)

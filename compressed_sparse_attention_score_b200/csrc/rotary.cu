@@ -95,7 +95,8 @@ __device__ __forceinline__ void pack8(const float (&f)[8], Eight<uint16_t> &v) {
 // Heads in units of eight values, 16-byte aligned: one block per token and `hpb` heads.  A unit is eight
 // neighbouring dims, or (HALF, turned dims) eight and the eight that they are paired with.  The token's cosines and
 // sines are formed once per block, in shared memory, while the first units' loads are under way; four units
-// are in flight per thread.  Bound by memory: every value once in, once out.
+// are in flight per thread.  Bound by memory: every value once in, once out (8192 x 64 heads of 512 bf16, 64 turned:
+// 168 us, 98 % of the copy rate; one value a thread 752 us; 1021 x 64 x 512 fp32 to bf16 37 us, 83 %).
 template <typename TX, typename TO, bool HALF>
 __global__ void __launch_bounds__(256) rotate8_kernel(RotateArgs a, int hpb, int units, uint32_t magic) {
   extern __shared__ float2 table[];
