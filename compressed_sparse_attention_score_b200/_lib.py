@@ -439,6 +439,15 @@ def _on(t, stream):
     return index, _raw_stream(index) if stream is None else stream.cuda_stream
 
 
+def _new(shape, dtype, device, stream):
+    """A tensor from the call's stream's memory (memory of another stream could still be in use there, or be given away
+    before this call has run)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _at(t, index, shape, dtype, what):
     """The pointer of a contiguous tensor of this device, shape and type (None: NULL)."""
     if t is None:
@@ -477,7 +486,7 @@ def csa2_rotate(x, pos, rotary, inverse=False, out=None, out_dtype=None, stream=
         raise ValueError("x must have a heads and a dim axis")
     index, s = _on(x, stream)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
+        out = _new(shape, out_dtype or x.dtype, x.device, stream)
     elif out.shape != shape or out.get_device() != index:
         raise ValueError("out must be shaped like x, on its device")
     xd, od = DTYPE.get(x.dtype), DTYPE.get(out.dtype)
@@ -568,11 +577,11 @@ def csa2_prefix_attn(q, q_pos, cache, softmax_scale, max_entries, prefix_entries
     i, s = _on(q, stream)
     heads = (B, Q, HEADS, MAIN_DIM)
     if o is None:
-        o = torch.empty(heads, dtype=o_dtype, device=q.device)
+        o = _new(heads, o_dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Q, HEADS), dtype=torch.float32, device=q.device)
+        lse = _new((B, Q, HEADS), torch.float32, q.device, stream)
     if ws is None:
-        ws = torch.empty(max(csa2_prefix_workspace_size(B, Q, max_entries), 1), dtype=torch.uint8, device=q.device)
+        ws = _new(max(csa2_prefix_workspace_size(B, Q, max_entries), 1), torch.uint8, q.device, stream)
     elif ws.get_device() != i:
         raise ValueError("ws must be on the device of the call's other tensors")
     R = 0 if swa_codes is None else swa_codes.shape[1]

@@ -99,7 +99,8 @@ __device__ __forceinline__ int64_t cache_slot(const csa2_cache &c, int b, int64_
 // Entries visible to a query at position pos of sequence b.
 __device__ __forceinline__ int visible_entries(const csa2_cache &c, int b, int pos) {
   int n = c.num_entries[b];
-  int by_pos = pos < 0 ? 0 : (pos + 1) / c.ratio;
+  // (unsigned: pos + 1 may be 2^31)
+  int by_pos = pos < 0 ? 0 : int(min((uint32_t(pos) + 1u) / uint32_t(c.ratio), 0x7FFFFFFFu));
   return min(n, by_pos);
 }
 

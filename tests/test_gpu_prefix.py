@@ -448,3 +448,50 @@ def test_very_large_and_very_small_logits():
                 vals = [torch.cat((torch.from_numpy(t.prefix).to(DEV), torch.from_numpy(t.values[b]).to(DEV))) for b in range(B)]
                 wo = torch.stack([torch.softmax(x[b], -1) @ vals[b] for b in range(B)])
                 check(o, lse, (to_np(wo), to_np(lse.double())), f"tau {tau}")
+
+
+def test_memory_of_its_own_on_another_stream():
+    """Outputs and a workspace that the call makes itself, for a stream that is not the current one: what the current
+    stream allocates and fills right after it does not get into them."""
+    t = Batch(2000, [5, 0, 33], 4, 16, 128, 1, seed=31)
+    want = t.run()
+    side = torch.cuda.Stream()
+    n = K().csa2_prefix_workspace_size(t.B, t.Q, t.most)
+    for _ in range(5):
+        torch.cuda.synchronize()
+        o, lse = t.run(stream=side)
+        for _ in range(3):
+            torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_the_last_position_and_single_entry_pages():
+    """Position 2^31 - 1 sees every entry, and a window that is in the ring by position; pages of one entry."""
+    t = Batch(150, [4, 70], 1, 1, 0, 1, seed=32)
+    o, lse = t.run()
+    for b in range(2):
+        check(o[b, 0], lse[b, 0], t.want(b, 0), f"b={b}")
+    t.q_pos.fill_(2 ** 31 - 1)
+    o2, lse2 = t.run()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and K().csa2_check(t.err) == 0
+
+
+def test_entries_behind_four_gigabytes():
+    """A prefix and own entries in a cache whose planes pass 2^32 bytes, in pages at its end."""
+    t = Batch(300, [40, 7], 4, 256, 0, 1, seed=33)
+    want = t.run()
+    page = t.cache.page_size
+    far = (1 << 24) // page + 5  # 2^24 entries of 256 code bytes
+    used = t.cache.num_slots // page
+    big = K().GlobalKVCache(t.B, 4, num_slots=(far + used) * page, page_table=t.table + far, page_size=page,
+                            num_entries=t.cache.num_entries)
+    for new, old in zip(big.planes, t.cache.planes):
+        new[far * page:] = old
+    o, lse = K().csa2_prefix_attn(t.q, t.q_pos, big, TAU, t.most, t.S, err=t.err)
+    assert K().csa2_check(t.err) == 0 and torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    t.cache = big
+    o, lse = K().csa2_prefix_attn(t.q[:, :1].repeat(1, 250, 1, 1).contiguous(), t.q_pos.repeat(1, 250).contiguous(), big, TAU,
+                                  t.most, t.S, err=t.err)  # (dequantised ahead)
+    for b in range(2):
+        check(o[b, 249], lse[b, 249], t.want(b, 0), f"ahead b={b}")

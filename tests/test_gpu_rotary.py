@@ -339,3 +339,47 @@ def test_captured_and_on_another_stream():
             want = R.pack_entries(to_np(kv[b])[None], to_np(ix[b])[None], e, 1, rot_args(rk), rot_args(ri))
             for x, y in zip(planes_of(cache, b, np.array([e]))[0], want):
                 np.testing.assert_array_equal(x, y)
+
+
+def test_offsets_behind_four_gigabytes():
+    """Tokens 2^31 values apart; entries, appended tokens and their groups in pages behind 2^32 bytes of the planes."""
+    k = K()
+    rk, ri = rotations("tail64")
+    far = (1 << 31) + 64
+    pos = torch.tensor([77, 900001], device=DEV, dtype=torch.int32)
+    x = torch.empty(far + 3 * 512, dtype=torch.bfloat16, device=DEV).as_strided((2, 3, 512), (far, 512, 1))
+    x.copy_(make((2, 3, 512), 1, torch.bfloat16))
+    got = k.csa2_rotate(x, pos, rk)
+    check_rotated(got, x.contiguous(), pos, rk)
+    x.zero_()
+    assert k.csa2_rotate(got, pos, rk, out=x) is x
+    assert torch.equal(x.contiguous(), k.csa2_rotate(got, pos, rk))
+    del x
+    page, n = 256, (1 << 24) // 256 + 3
+    cache = k.GlobalKVCache(2, 1, num_slots=(n + 4) * page, page_size=page,
+                            page_table=torch.tensor([[n, n + 2], [n + 3, n + 1]], dtype=torch.int32, device=DEV))
+    kv, ix = make((2, 300, 512), 2, torch.bfloat16), make((2, 300, 128), 3, torch.bfloat16)
+    k.csa2_pack_kv_rotary(kv, ix, torch.zeros(2, dtype=torch.int32, device=DEV), cache, rk, ri, err=(err := err_word()))
+    last = make((2, 512), 4, torch.bfloat16), make((2, 128), 5, torch.bfloat16)
+    k.csa2_append_kv_rotary(*last, torch.full((2,), 300, dtype=torch.int32, device=DEV), cache, rk, ri, err=err)
+    assert k.csa2_check(err) == 0 and cache.num_entries.tolist() == [301, 301]
+    for b in range(2):
+        rows = torch.cat((kv[b], last[0][b:b + 1])), torch.cat((ix[b], last[1][b:b + 1]))
+        want = R.pack_entries(to_np(rows[0]), to_np(rows[1]), 0, 1, rot_args(rk), rot_args(ri))
+        for got, w in zip(planes_of(cache, b, np.arange(301))[0], want):
+            np.testing.assert_array_equal(got, w)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_results_on_a_stream_of_their_own(dtype):
+    """A new output for a stream that is not the current one."""
+    k = K()
+    rk, _ = rotations("tail64")
+    x, pos = make((500, 64, 512), 6, dtype), torch.arange(500, device=DEV, dtype=torch.int32)
+    want = k.csa2_rotate(x, pos, rk)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = k.csa2_rotate(x, pos, rk, stream=side)
+    torch.full_like(x, 3.0)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
