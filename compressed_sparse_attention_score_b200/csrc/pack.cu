@@ -110,14 +110,29 @@ __device__ __forceinline__ uint4 hat8(uint32_t codes, uint32_t s16) {
   return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-// x / s rounded to nearest, for r = 1 / s rounded to nearest and results and remainders in normal range: an estimate corrected
-// by its exact remainder.  The corrected value is within 2^-23 ulp of the quotient before it is rounded; where s has few
-// significant bits (E4M3: four) no quotient is that close to the middle of two numbers (at least 1/30 ulp: the distance is a
+// x / s rounded to nearest, for r within an ulp of 1 / s and results and remainders in normal range: an estimate corrected
+// by its exact remainder.  The corrected value is within 2^-21 ulp of the quotient before it is rounded; where s has few
+// significant bits (E4M3: four; 6: two) no quotient is that close to the middle of two numbers (at least 1/30 ulp: the distance is a
 // multiple of 1 / 2 s in units of the numbers' last places), so one correction is enough.  __fdiv_rn, which takes every
 // case, is three times as long.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
   const float q = __fmul_rn(x, r);
   return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+}
+// 1 / s within an ulp.
+__device__ __forceinline__ float rcp_estimate(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+// Two quotients by packed operations, half the instructions.
+__device__ __forceinline__ void quotient2(const float *x, float s, float r, float *q) {
+  asm("{\n\t.reg .b64 x, r, s, q, e;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 r, {%4, %4};\n\tmov.b64 s, {%5, %5};\n\t"
+      "mul.rn.f32x2 q, x, r;\n\tfma.rn.f32x2 e, q, s, x;\n\tfma.rn.f32x2 q, e, r, q;\n\t"
+      "mov.b64 {%0, %1}, q;\n\t}"
+      : "=f"(q[0]), "=f"(q[1])
+      : "f"(x[0]), "f"(x[1]), "f"(r), "f"(-s));
 }
 // The same for any s: the second correction starts from an estimate within one ulp, from which q + r (x - s q) is the
 // rounded quotient (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).
@@ -131,7 +146,7 @@ __device__ __forceinline__ float quotient_any(float x, float s, float r) {
 __device__ __forceinline__ uint32_t codes8(const float *x, float s, float r) {
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = quotient(x[i], s, r);
+  for (int i = 0; i < 8; i += 2) quotient2(x + i, s, r, q + i);
   uint32_t w;  // (the conversion puts its first operand in the high nibble)
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
@@ -143,10 +158,10 @@ __device__ __forceinline__ uint32_t codes8(const float *x, float s, float r) {
   return w & (0x77777777u | (m << 3));
 }
 
-// max(a, |b|), NaN if either is.
-__device__ __forceinline__ float max_abs_nan(float a, float b) {
+// max(|a|, |b|, |c|), NaN if one is.
+__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
   float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
@@ -158,9 +173,9 @@ __device__ __forceinline__ void store_entry(const float (&x)[16], const float (&
                                             uint16_t *ix_hat = nullptr) {
   float amax = 0.f, am = 0.f;  // (NaN if a value is)
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = max_abs_nan(amax, x[i]);
+  for (int i = 0; i < 16; i += 2) amax = max_abs_nan(amax, x[i], x[i + 1]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) am = max_abs_nan(am, xi[i]);
+  for (int i = 0; i < 4; i += 2) am = max_abs_nan(am, xi[i], xi[i + 1]);
   // values that are not finite, or nearly not, take the general divisions
   const bool special = __any_sync(0xffffffffu, !(amax < 0x1p126f) || !(am < 0x1p126f));
   if (special) {
@@ -170,50 +185,55 @@ __device__ __forceinline__ void store_entry(const float (&x)[16], const float (&
 #pragma unroll
     for (int i = 0; i < 4; ++i) am = fmaxf(am, fabsf(xi[i]));
   }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
 
-  // ---- main KV: E4M3 scale per 16 values, e2m1 codes
-  const uint32_t sc = e4m3_code(__fdiv_rn(amax, 6.0f));
-  const float s = e4m3_value(sc);
-  uint32_t lo = 0, hi = 0;
+  // Main KV: E4M3 scale per 16 values, e2m1 codes; indexer key: E8M0 exponent per 32 values (8 lanes), e2m1 codes.
+  uint32_t sc, s16, lo, hi, code4;
+  int ex;
+  auto scale = [&](float q) {
+    sc = e4m3_code(q);
+    s16 = sm100::cvt_e4m3x2_f16x2(sc * 0x101u);
+    return __half2float(__ushort_as_half(uint16_t(s16)));
+  };
   if (special) {
+    const float s = scale(__fdiv_rn(amax, 6.0f));
+    lo = hi = code4 = 0;
     if (s != 0.f) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) lo |= e2m1_code(__fdiv_rn(x[i], s)) << (4 * i);
 #pragma unroll
       for (int i = 0; i < 8; ++i) hi |= e2m1_code(__fdiv_rn(x[8 + i], s)) << (4 * i);
     }
-  } else if (s != 0.f) {  // (a quotient below 2^-126 is code 0 whatever its last bits)
-    const float r = __frcp_rn(s);
-    lo = codes8(x, s, r);
-    hi = codes8(x + 8, s, r);
-  }
-  reinterpret_cast<uint2 *>(c.kv_codes + slot * CSA2_MAIN_CODE_BYTES)[lane] = make_uint2(lo, hi);
-  c.kv_scales[slot * CSA2_MAIN_SCALE_BYTES + lane] = uint8_t(sc);
-  if (kv_hat) {
-    const uint32_t s16 = sm100::cvt_e4m3x2_f16x2(sc * 0x101u);
-    reinterpret_cast<uint4 *>(kv_hat)[2 * lane] = hat8(lo, s16);
-    reinterpret_cast<uint4 *>(kv_hat)[2 * lane + 1] = hat8(hi, s16);
-  }
-
-  // ---- indexer key: E8M0 exponent per 32 values (8 lanes), e2m1 codes
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-  uint32_t code4 = 0;
-  int ex = -127;
-  if (am != 0.f) {
-    ex = e8m0_ceil_exponent(__fdiv_rn(am, 6.0f));
-    if (special) {
+    ex = -127;
+    if (am != 0.f) {
+      ex = e8m0_ceil_exponent(__fdiv_rn(am, 6.0f));
       const float si = pow2f(ex);
 #pragma unroll
       for (int i = 0; i < 4; ++i) code4 |= e2m1_code(__fdiv_rn(xi[i], si)) << (4 * i);
-    } else {
-      const float by = pow2f(-ex);  // (a power of two: the product is the quotient)
-      code4 = sm100::e2m1x2_code(xi[0] * by, xi[1] * by) | sm100::e2m1x2_code(xi[2] * by, xi[3] * by) << 8;
-      code4 &= 0x7777u | ((code4 | (code4 >> 1) | (code4 >> 2)) & 0x1111u) << 3;
     }
+  } else {
+    // (below 2^-100 the estimate's last bits may be off, but the code is 0 either way)
+    const float s = scale(quotient(amax, 6.0f, 1.0f / 6.0f));
+    // (a quotient below 2^-126 is code 0 whatever its last bits; a scale of 0 leaves none)
+    const float r = rcp_estimate(s);
+    lo = codes8(x, s, r), hi = codes8(x + 8, s, r);
+    if (s == 0.f) lo = hi = 0;
+    // 2^ex >= am / 6 is 1.5 x 2^(ex + 2) >= am, which the bits of am tell, down to where the quotient would be subnormal
+    ex = int((__float_as_uint(am) + 0x3FFFFFu) >> 23) - 129;
+    if (am < 0x1p-120f) ex = e8m0_ceil_exponent(__fdiv_rn(am, 6.0f));  // (-127 for 0)
+    const float by = pow2f(-ex);  // (a power of two: the product is the quotient)
+    code4 = sm100::e2m1x2_code(xi[0] * by, xi[1] * by) | sm100::e2m1x2_code(xi[2] * by, xi[3] * by) << 8;
+    code4 &= 0x7777u | ((code4 | (code4 >> 1) | (code4 >> 2)) & 0x1111u) << 3;
   }
+  reinterpret_cast<uint2 *>(c.kv_codes + slot * CSA2_MAIN_CODE_BYTES)[lane] = make_uint2(lo, hi);
+  c.kv_scales[slot * CSA2_MAIN_SCALE_BYTES + lane] = uint8_t(sc);
   reinterpret_cast<uint16_t *>(c.ix_codes + slot * CSA2_IX_CODE_BYTES)[lane] = uint16_t(code4);
   if ((lane & 7) == 0) c.ix_scales[slot * CSA2_IX_SCALE_BYTES + (lane >> 3)] = uint8_t(ex + 127);
+  if (kv_hat) {
+    reinterpret_cast<uint4 *>(kv_hat)[2 * lane] = hat8(lo, s16);
+    reinterpret_cast<uint4 *>(kv_hat)[2 * lane + 1] = hat8(hi, s16);
+  }
   if (ix_hat) {
     const float si = pow2f(ex);
     reinterpret_cast<uint2 *>(ix_hat)[lane] = make_uint2(hat2(code4 & 0xFF, 0x3C003C00u, si), hat2(code4 >> 8, 0x3C003C00u, si));
@@ -290,7 +310,7 @@ __device__ __forceinline__ void turn_values(float (&x)[16], float (&xi)[4], cons
 }
 
 // cos and sin of a pair at a position that goes up in equal steps: each is the last one turned by a step's angle (an error of
-// 2^-53 a step; a new start after at most 16).
+// 2^-53 a step; a new start after at most 64).
 struct Turning {
   double2 at, by;
   __device__ __forceinline__ void start(uint64_t step, int64_t pos) { at = rotary_cs64(step, pos); }
@@ -419,18 +439,24 @@ __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_
 
 // The rotating pack of a chunk whose main and indexer values share one table of at most 32 pairs: a warp takes `run`
 // consecutive entries (lanes as in pack_kv_kernel; lane l turns pair l), so that a sine and cosine in fp64 serve a run, and asks
-// for the next entry's first token before it quantises this one.  Bound by instruction issue (about 570 a warp and
-// entry): 131288 bf16 tokens, r = 1, with the values stored, 100 us (58 % of the copy rate; a sine and cosine per
-// entry 162 us).
+// for the next entry's first token before it quantises this one.  Bound by instruction issue (about 440 a warp and
+// entry) and what of its latencies 24 warps an SM leave: 131288 bf16 tokens, r = 1, with the values stored, 82 us (71 % of
+// the copy rate; a sine and cosine per entry 162 us); 64000 fp32 tokens 49 us.  Blocks are as many as leave
+// registers enough: with 64 a thread, 32 warps an SM, a few spilled values made it 99 us (fp32, 80 a thread: 65 us).
+constexpr int64_t PACK_RUN = 64;  // entries that a warp takes at most
 template <typename T>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 3)
+constexpr int PACK_WARPS = sizeof(T) == 2 ? 8 : 4;  // of a block
+template <typename T>
+constexpr int PACK_BLOCKS = sizeof(T) == 2 ? 3 : 5;  // on an SM
+template <typename T>
+__global__ void __launch_bounds__(32 * PACK_WARPS<T>, PACK_BLOCKS<T>)
     pack_run_kernel(const T *__restrict__ lat_kv, const T *__restrict__ lat_ix, const float *__restrict__ pool_w, int T_,
                     int n_new, int64_t all, int run, const int32_t *__restrict__ first_entry, csa2_cache c, RotaryWrite rw,
                     int32_t *err) {
-  __shared__ float turn_buf[8][TURN_ROW];
+  __shared__ float turn_buf[PACK_WARPS<T>][TURN_ROW];
   const int lane = threadIdx.x & 31, r = c.ratio;
   float *buf = turn_buf[threadIdx.x >> 5];
-  int64_t e = (int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5)) * run;
+  int64_t e = (int64_t(blockIdx.x) * PACK_WARPS<T> + (threadIdx.x >> 5)) * run;
   int left = int(min(int64_t(run), all - e));
   if (left <= 0) return;
   int b = int(e / n_new), j = int(e % n_new);
@@ -635,9 +661,11 @@ static void pack_kv(const void *lat_kv, const void *lat_ix, const float *pool_w,
   const int64_t n = int64_t(B) * (T_ / c.ratio);
   if (n == 0) return;
   if (ROT && !gate_kv && (rw.same || !rw.kv.rot_dim || !rw.ix.rot_dim) && rw.kv.rot_dim <= 64 && rw.ix.rot_dim <= 64) {
-    // runs of up to 16 entries, as long as every SM still gets 16 warps
-    const int run = int(std::min<int64_t>(16, std::max<int64_t>(1, n / (int64_t(sm_count()) * 16))));
-    pack_run_kernel<T><<<unsigned((n + 8 * run - 1) / (8 * run)), 256, 0, st>>>(
+    // runs of up to PACK_RUN entries, of a length that fills the device a whole number of times
+    const int64_t fit = int64_t(sm_count()) * PACK_WARPS<T> * PACK_BLOCKS<T>;  // warps at once
+    const int64_t rounds = (n + PACK_RUN * fit - 1) / (PACK_RUN * fit);
+    const int run = int((n + rounds * fit - 1) / (rounds * fit));
+    pack_run_kernel<T><<<unsigned((n + PACK_WARPS<T> * run - 1) / (PACK_WARPS<T> * run)), 32 * PACK_WARPS<T>, 0, st>>>(
         static_cast<const T *>(lat_kv), static_cast<const T *>(lat_ix), pool_w, T_, T_ / c.ratio, n, run, first_entry, c, rw, err);
     return;
   }

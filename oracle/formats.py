@@ -121,14 +121,14 @@ def e4m3_encode(v):
 
 # --------------------------------------------------------------------------- E8M0
 def e8m0_ceil_exponent(q):
-    """ceil(log2 q) for fp32 q > 0, clamped to the E8M0 range [-127, 127].
+    """ceil(log2 q) for fp32 q >= 0, clamped to the E8M0 range [-127, 127] (0, an underflown quotient among them: -127).
 
     frexp gives q = f * 2^x with f in [0.5, 1); log2 q is x - 1 exactly when
     f == 0.5 and lies strictly inside (x - 1, x) otherwise.
     """
     q = np.asarray(q, dtype=F32).astype(np.float64)
     f, x = np.frexp(q)
-    e = np.where(f == 0.5, x - 1, x)
+    e = np.where(q == 0, -127, np.where(f == 0.5, x - 1, x))
     return np.clip(e, -127, 127).astype(np.int64)
 
 

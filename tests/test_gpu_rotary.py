@@ -227,6 +227,60 @@ def test_pack_bytes(ratio, page, B, T, first, dtype, kind, pooling):
         assert (to_np(p)[~touched] == 0xA5).all()  # nothing else is written
 
 
+def scale_border_latents():
+    """fp32 latents whose blocks' largest values are 6 times a border between two scales, or a neighbour of that, from
+    subnormal ones to 2^125, and whose other values are at or next to borders between two codes of such a scale."""
+    rng = np.random.default_rng(7)
+    f = np.float32
+
+    def neighbours(v):
+        v = np.asarray(v, f)
+        return np.concatenate([np.nextafter(v, f(0)), v, np.nextafter(v, f(np.inf))])
+
+    with np.errstate(over="ignore"):
+        step = np.unique(np.concatenate([np.arange(0, 16) * 2.0 ** -9, *(np.arange(8, 16) * 2.0 ** e for e in range(-9, 6))]))
+    step = step[step <= 448]
+    main = neighbours(6 * np.concatenate([step, (step[1:] + step[:-1]) / 2]))
+    main = main[main > 0]
+    index = neighbours(np.ldexp(f(6), np.arange(-150, 123)))
+    index = index[index > 0]
+    entries = max(-(-len(main) // 32), -(-len(index) // 4))
+    kv, ix = np.zeros((entries, 512), f), np.zeros((entries, 128), f)
+    border = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], f)
+    for x, tops, width in ((kv, main, 16), (ix, index, 32)):
+        for n, top in enumerate(tops):
+            e, at = divmod(n, x.shape[1] // width)
+            scale = F.e4m3_decode(F.e4m3_encode(f(top) / f(6))) if width == 16 else np.ldexp(1.0, int(F.e8m0_ceil_exponent(np.array([f(top) / f(6)], f))[0]))
+            v = neighbours((np.float64(scale) * border[rng.integers(0, 7, 16)]).astype(f))
+            v = np.minimum(rng.permutation(v)[:width] * rng.choice([-1, 1], width), top).astype(f)
+            v = np.where(np.abs(v) > top, top, v)
+            v[rng.integers(0, width)] = top * rng.choice([-1, 1])
+            x[e, width * at:width * (at + 1)] = v
+    return kv, ix
+
+
+def test_pack_at_the_borders_of_scales_and_codes():
+    k = K()
+    kv, ix = scale_border_latents()
+    E = kv.shape[0]
+    (mc, ms), (xc, xs) = F.pack_main(kv), F.pack_indexer(ix)
+    zero = torch.zeros(1, dtype=torch.int32, device=DEV)
+    a, b = torch.from_numpy(kv)[None].to(DEV), torch.from_numpy(ix)[None].to(DEV)
+    turned = k.Rotary(torch.zeros(64, dtype=torch.int64, device=DEV))  # angles of 0: the values stay
+    two = k.Rotary(torch.zeros(32, dtype=torch.int64, device=DEV))
+    for kind in ("plain", "runs", "single", "append"):
+        cache, err = new_cache(E if kind == "append" else 1, 1, 1 if kind == "append" else E), err_word()
+        if kind == "plain":
+            k.csa2_pack_kv(a, b, zero, cache, err=err)
+        elif kind == "append":
+            k.csa2_append_kv_rotary(a[0], b[0], torch.zeros(E, dtype=torch.int32, device=DEV), cache, turned, two, err=err)
+        else:
+            k.csa2_pack_kv_rotary(a, b, zero, cache, two if kind == "runs" else turned, two, err=err)
+        assert k.csa2_check(err) == 0
+        for plane, want in zip(cache.planes, (mc, ms, xc, xs)):
+            assert (to_np(plane).reshape(E, -1) == np.asarray(want).reshape(E, -1)).all(), kind
+
+
 def test_pack_without_rotations_is_the_plain_pack():
     k = K()
     kv, ix = make((2, 40, 512), 1, torch.bfloat16), make((2, 40, 128), 2, torch.bfloat16)

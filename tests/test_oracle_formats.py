@@ -191,3 +191,12 @@ def test_entry_sizes_match_pages():
     assert F.MAIN_SCALE_BYTES == g["main_entry"]["scale_bytes"]
     assert F.IX_SCALE_BYTES == g["indexer_entry"]["scale_bytes"]
     assert F.MAIN_ENTRY_BYTES + F.IX_ENTRY_BYTES == g["bytes_per_entry_pair"]["value"]
+
+
+def test_e8m0_of_values_whose_sixth_underflows():
+    """2^-149 / 6 is 0 in fp32: the block keeps the least scale, 2^-127, as a block of zeros does."""
+    x = np.zeros((4, 128), np.float32)
+    x[1, :32], x[2, 5], x[3, 127] = np.float32(2.0 ** -149), np.float32(-(2.0 ** -148)), np.float32(2.0 ** -126)
+    codes, scales = F.pack_indexer(x)
+    assert (scales == 0).all()
+    assert (codes[:3] == 0).all() and codes[3, 63] == 0x40  # (2^-126 is two steps of 2^-127: code 4, in the high nibble)
