@@ -27,8 +27,8 @@
 // tile has 64 of them, and its 128 KB are written there too: 4150 clocks a tile, 4850 measured (2.75 us; 4.9 us where the
 // tile is dequantised in the block).  The rest is the softmax between a tile's products; TMEM and shared memory
 // hold one row's tile, so nothing else can run meanwhile.
-// Measured (whole call): 32 rows over 8192 shared entries 73 us, 96 over 4096 100 us, 16 over 65536 216 us (641
-// TFLOP/s), 13 over 2999 36 us, 2 over 96 23 us.
+// Measured (whole call): 32 rows over 8192 shared entries 70 us, 96 over 4096 98 us, 16 over 65536 208 us (665
+// TFLOP/s), 13 over 2999 34 us, 2 over 96 21 us.
 #include <cuda_fp16.h>
 #include <string.h>
 
@@ -45,8 +45,9 @@ constexpr int PX_TILE = 128;                 // keys per tile
 constexpr int PX_PROD = 256, PX_SOFT = 256;  // producer and softmax threads (warps 0-7, 8-15)
 constexpr int PX_ISSUE_WARP = 16, PX_LOAD_WARP = 17;
 constexpr int PX_THREADS = PX_PROD + PX_SOFT + 128;  // (the last warpgroup has two working warps)
-// Registers per thread after launch (96 x 640): 256 x 96 + 256 x 120 + 128 x 48 = 61440.
-constexpr int PX_REG_SOFT = 120, PX_REG_ISSUE = 48;
+// Registers per thread after launch (96 x 640): 256 x 96 + 256 x 128 + 128 x 32 = 61440.  (Softmax warps with 120
+// spill more: 16 rows over 65536 shared entries 217 against 211 us.)
+constexpr int PX_REG_SOFT = 128, PX_REG_ISSUE = 32;
 static_assert(PX_PROD * 96 + PX_SOFT * PX_REG_SOFT + 128 * PX_REG_ISSUE <= 96 * PX_THREADS,
               "the warpgroups' registers exceed the block's");
 // A shared prefix is dequantised ahead where at least this many rows have at least this many tiles of it in all (2.7 tiles a
@@ -228,7 +229,9 @@ struct KeyPart {
   uint32_t slot[2];  // cache slot of an entry, ring slot of a window token; NO_SLOT: no key
   int entries;       // keys of the tile below this are entries
   float scale[2];    // a window token's scale
-  uint4 raw[2][2];   // in one pair of blocks, an entry's 32 codes [0] and two scales [1].x, or a token's 32 codes
+};
+struct KeyBytes {
+  uint4 raw[2][2];  // in one pair of blocks, an entry's 32 codes [0] and two scales [1].x, or a token's 32 codes
 };
 struct KeyPlace {
   int key0;   // the first of its keys
@@ -261,17 +264,17 @@ __device__ __forceinline__ void find_keys(const PrefixArgs &p, const Work &w, co
 }
 
 // The keys' bytes of pair d.
-__device__ __forceinline__ void load_keys(const PrefixArgs &p, const KeyPlace &at, int d, KeyPart &r) {
+__device__ __forceinline__ void load_keys(const PrefixArgs &p, const KeyPlace &at, int d, const KeyPart &r, KeyBytes &x) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (r.slot[i] == NO_SLOT) continue;
     if (at.key0 + 8 * i < r.entries) {
-      r.raw[i][0] = *reinterpret_cast<const uint4 *>(p.c.kv_codes + int64_t(r.slot[i]) * CSA2_MAIN_CODE_BYTES + 64 * d + at.piece * 16);
-      r.raw[i][1].x = *reinterpret_cast<const uint16_t *>(p.c.kv_scales + int64_t(r.slot[i]) * CSA2_MAIN_SCALE_BYTES + 8 * d + at.piece * 2);
+      x.raw[i][0] = *reinterpret_cast<const uint4 *>(p.c.kv_codes + int64_t(r.slot[i]) * CSA2_MAIN_CODE_BYTES + 64 * d + at.piece * 16);
+      x.raw[i][1].x = *reinterpret_cast<const uint16_t *>(p.c.kv_scales + int64_t(r.slot[i]) * CSA2_MAIN_SCALE_BYTES + 8 * d + at.piece * 2);
     } else {
       const uint4 *src = reinterpret_cast<const uint4 *>(p.codes + int64_t(r.slot[i]) * CSA2_SWA_DIM + 128 * d + 32 * at.piece);
-      r.raw[i][0] = src[0];
-      r.raw[i][1] = src[1];
+      x.raw[i][0] = src[0];
+      x.raw[i][1] = src[1];
     }
   }
 }
@@ -287,42 +290,36 @@ __device__ __forceinline__ void store_factors(const KeyPlace &at, const KeyPart 
   }
 }
 
-// Those 32 dims of the keys in fp16, times 2^-7, in the order of unpack8.
-__device__ __forceinline__ void dequant_keys(const KeyPlace &at, const KeyPart &r, uint32_t (&h)[32]) {
+// Key i's 32 dims in fp16, times 2^-7, in the order of unpack8.
+__device__ __forceinline__ void dequant_key(const KeyPlace &at, const KeyPart &r, const KeyBytes &x, int i, uint32_t (&h)[16]) {
+  const uint4 a = x.raw[i][0], b = x.raw[i][1];
+  if (r.slot[i] == NO_SLOT) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t *hk = h + 16 * i;
-    const uint4 a = r.raw[i][0], b = r.raw[i][1];
-    if (r.slot[i] == NO_SLOT) {
+    for (int e = 0; e < 16; ++e) h[e] = 0u;
+  } else if (at.key0 + 8 * i < r.entries) {
+    const uint32_t s0 = scale128(b.x & 0xFFu), s1 = scale128(b.x >> 8);
+    unpack8(a.x, s0, h);
+    unpack8(a.y, s0, h + 4);
+    unpack8(a.z, s1, h + 8);
+    unpack8(a.w, s1, h + 12);
+  } else {
+    const __half2 two = __float2half2_rn(pow2f(window_exponent(r.scale[i]) - 7));
+    const uint32_t s = *reinterpret_cast<const uint32_t *>(&two);
+    const uint32_t w8[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int e = 0; e < 16; ++e) hk[e] = 0u;
-    } else if (at.key0 + 8 * i < r.entries) {
-      const uint32_t s0 = scale128(b.x & 0xFFu), s1 = scale128(b.x >> 8);
-      unpack8(a.x, s0, hk);
-      unpack8(a.y, s0, hk + 4);
-      unpack8(a.z, s1, hk + 8);
-      unpack8(a.w, s1, hk + 12);
-    } else {
-      const __half2 two = __float2half2_rn(pow2f(window_exponent(r.scale[i]) - 7));
-      const uint32_t s = *reinterpret_cast<const uint32_t *>(&two);
-      const uint32_t w8[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    for (int v = 0; v < 4; ++v)
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          hk[4 * v + e] = hmul2_u32(cvt_e4m3x2_f16x2(__byte_perm(w8[2 * v], w8[2 * v + 1], e | ((4 + e) << 4)) & 0xFFFF), s);
-    }
+      for (int e = 0; e < 4; ++e)
+        h[4 * v + e] = hmul2_u32(cvt_e4m3x2_f16x2(__byte_perm(w8[2 * v], w8[2 * v + 1], e | ((4 + e) << 4)) & 0xFFFF), s);
   }
 }
 
 // Those values into the pair of blocks at dst.
-__device__ __forceinline__ void store_keys(const uint32_t (&h)[32], const KeyPlace &at, uint8_t *dst) {
+__device__ __forceinline__ void store_key(const uint32_t (&h)[16], const KeyPlace &at, int i, uint8_t *dst) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-      *reinterpret_cast<uint4 *>(dst + (at.piece >> 1) * 16384 + kmaj128(at.key0 + 8 * i, 4 * (at.piece & 1) + v)) =
-          make_uint4(h[16 * i + 4 * v], h[16 * i + 4 * v + 1], h[16 * i + 4 * v + 2], h[16 * i + 4 * v + 3]);
+  for (int v = 0; v < 4; ++v)
+    *reinterpret_cast<uint4 *>(dst + (at.piece >> 1) * 16384 + kmaj128(at.key0 + 8 * i, 4 * (at.piece & 1) + v)) =
+        make_uint4(h[4 * v], h[4 * v + 1], h[4 * v + 2], h[4 * v + 3]);
 }
 
 // One block of 64 dims of the prefix's tile `tile` into shared memory, completing on `bar`.
@@ -483,14 +480,17 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
 
   if (p.shared == 0) grid_dep_wait();  // (the inputs may be the previous kernel's work)
   // ---- the plan: the tiles of all rows and of the longest, and this block's share
-  int *first = scan + 36;  // this block's first row, first tile of it, shared tiles, longest row
-  int sum = 0, most = 0, copied_tiles = 0;
+  int *first = scan + 36;  // this block's first row, first tile of it, shared tiles, longest row, its tiles (2), the row's keys (5)
+  auto first_row = [&](int row, int tile, const RowKeys &k) {
+    first[0] = row, first[1] = tile;
+    first[6] = k.b, first[7] = k.nks, first[8] = k.lo, first[9] = k.nk, first[10] = k.tiles;
+  };
+  RowKeys mine{};  // (read for up to 32 rows, a lane's own)
+  int sum = 0, most = 0;
   for (int row = tid; row < p.rows; row += PX_THREADS) {
-    const RowKeys k = row_keys(p, row);
-    const int n = k.tiles;
-    copied_tiles = min(p.shared, k.nks / PX_TILE);  // (read for up to 32 rows, a lane's own)
-    sum += n;
-    most = max(most, n);
+    mine = row_keys(p, row);
+    sum += mine.tiles;
+    most = max(most, mine.tiles);
     if (blockIdx.x == 0 && visible_entries(p.c, row / p.Q, p.q_pos[row]) > p.n_bound) report(p.err, CSA2_ERR_SHAPE);
   }
   // Up to 32 rows are counted by the first warp alone, which saves the block's barriers.
@@ -531,11 +531,11 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
       int row = by_row ? int(blockIdx.x) / parts : 0;
       if (by_row) {
         const int n = __shfl_sync(0xffffffffu, sum, row & 31), i = blockIdx.x % parts;
-        const int copied = __shfl_sync(0xffffffffu, copied_tiles, row & 31);
+        const int copied = __shfl_sync(0xffffffffu, min(p.shared, mine.nks / PX_TILE), row & 31);
         t0 = row < p.rows ? part_start(n, copied, i, parts) : 0, t1 = row < p.rows ? part_start(n, copied, i + 1, parts) : 0;
-        if (lane == 0) first[0] = row, first[1] = t0;
+        if (lane == row) first_row(row, t0, mine);
       } else if (sum > 0 && off <= t0 && t0 < off + sum) {
-        first[0] = lane, first[1] = t0 - off;
+        first_row(lane, t0 - off, mine);
       }
       if (lane == 0) first[4] = t0, first[5] = t1;
     }
@@ -549,16 +549,18 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
       if (row < p.rows) k = row_keys(p, row);
       const int copied = min(p.shared, k.nks / PX_TILE);
       t0 = part_start(k.tiles, copied, i, parts), t1 = part_start(k.tiles, copied, i + 1, parts);
-      if (tid == 0) first[0] = row, first[1] = t0;
+      if (tid == 0) first_row(row, t0, k);
     }
     if (!by_row || blockIdx.x == 0)
       for (int row0 = 0, base = 0; row0 < p.rows; row0 += PX_THREADS) {
         const int row = row0 + tid;
-        const int n = row < p.rows ? row_keys(p, row).tiles : 0;
+        RowKeys k{};
+        if (row < p.rows) k = row_keys(p, row);
+        const int n = k.tiles;
         int all = 0;
         const int off = base + block_exclusive_scan_1024(n, scan, &all);
         if (blockIdx.x == 0 && row < p.rows) p.plan[16 + row] = off;
-        if (!by_row && n > 0 && off <= t0 && t0 < off + n) first[0] = row, first[1] = t0 - off;
+        if (!by_row && n > 0 && off <= t0 && t0 < off + n) first_row(row, t0 - off, k);
         base += all;
         if (blockIdx.x != 0 && t0 < base) break;
       }
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
     grid_dep_wait();  // (so that this kernel's end implies the expansion's)
     return;
   }
-  if (!few) __syncthreads();  // first[0] and [1] are written
+  if (!few) __syncthreads();  // the first row is written
   if (tid < 512)  // the first query row on its way into L2 while the block is set up
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + int64_t(first[0]) * H * D + 64 * tid));
   // entries below `limit` are read from the workspace: the shared tiles before the first bad one
@@ -607,16 +609,17 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   const uint32_t tmem = *tmem_slot;
   Work w;
   w.row = first[0], w.tile = first[1], w.left = t1 - t0;
-  w.k = row_keys(p, w.row);
+  w.k = RowKeys{first[6], first[7], first[8], first[9], first[10]};
   const int limit = *limit_at * PX_TILE;
 
   if (warp < 8) {
     // ------------------------------------------------------------ producers: warp w keys 16 w .. + 15
-    // Each pair's values are dequantised into registers, and the next pair's bytes asked for, before the pair's blocks are
-    // free: only the stores lie between the last product that reads a block and the first that reads its successor.
+    // The next pair's bytes are asked for before a pair is dequantised, and its first key waits in registers for the pair's
+    // blocks to be free.
     const KeyPlace at{16 * warp + (lane & 3) + 4 * ((lane >> 3) & 1), ((lane >> 2) & 1) + 2 * (lane >> 4)};
     KeyPart r;
-    uint32_t h[32];
+    KeyBytes x, ahead;
+    uint32_t h[16];
     bool ok = true;
     int seen = -1;  // the last tile whose products are known to have read it all
     auto wait = [&](int d, int n) {
@@ -625,20 +628,24 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
     for (int n = 0; w.left > 0 && ok; ++n, w.next(p)) {
       if (w.within(limit)) continue;
       find_keys(p, w, at, r);
-      load_keys(p, at, 0, r);
+      load_keys(p, at, 0, r, x);
 #pragma unroll 1
       for (int d = 0; d < 4; ++d) {
-        dequant_keys(at, r, h);
-        if (d < 3) load_keys(p, at, d + 1, r);
+        if (d < 3) load_keys(p, at, d + 1, r, ahead);
+        dequant_key(at, r, x, 0, h);
         // (a barrier's parity tells only its last two phases apart: the loader's tiles in between are counted too)
         for (; ok && seen < n - 2; ++seen) ok = wait(3, seen + 1);
         if (ok && n > 0) ok = wait(d, n - 1);
         if (!ok) break;
         if (d == 0 && at.piece == 0) store_factors(at, r, mul + (n & 1) * 128);
-        store_keys(h, at, smem + PX_K + d * 2 * 16384);
+        uint8_t *dst = smem + PX_K + d * 2 * 16384;
+        store_key(h, at, 0, dst);
+        dequant_key(at, r, x, 1, h);
+        store_key(h, at, 1, dst);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[d]);
+        x = ahead;
       }
       seen = n - 1;
     }
