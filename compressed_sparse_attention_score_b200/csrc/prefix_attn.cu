@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   }
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&full[i], 8);
+      mbar_init(&full[i], i == 0 ? 9 : 8);  // the producer warps; the first pair's also the loader, whoever writes the tile
       mbar_init(&freed[i], 1);
     }
     mbar_init(s_full, 1);
@@ -621,21 +621,25 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
     KeyBytes x, ahead;
     uint32_t h[16];
     bool ok = true;
-    int seen = -1;  // the last tile whose products are known to have read it all
     auto wait = [&](int d, int n) {
       return __all_sync(0xffffffffu, mbar_wait_bounded(&freed[d], n & 1, abort_flag, PX_WAIT_NS));
     };
     for (int n = 0; w.left > 0 && ok; ++n, w.next(p)) {
-      if (w.within(limit)) continue;
+      if (w.within(limit)) {
+        // The loader's tile.  It counts these warps all the same: a barrier's parity tells only its last two phases apart, and
+        // as no tile's products begin before every writer has seen the tile before it freed, `freed` cannot run ahead of a
+        // writer that is late.  (Given up, the arrival still ends the phase that the loader's copies belong to.)
+        if (n > 0) ok = wait(0, n - 1);
+        if (lane == 0) mbar_arrive(&full[0]);
+        continue;
+      }
       find_keys(p, w, at, r);
       load_keys(p, at, 0, r, x);
 #pragma unroll 1
       for (int d = 0; d < 4; ++d) {
         if (d < 3) load_keys(p, at, d + 1, r, ahead);
         dequant_key(at, r, x, 0, h);
-        // (a barrier's parity tells only its last two phases apart: the loader's tiles in between are counted too)
-        for (; ok && seen < n - 2; ++seen) ok = wait(3, seen + 1);
-        if (ok && n > 0) ok = wait(d, n - 1);
+        if (n > 0) ok = wait(d, n - 1);
         if (!ok) break;
         if (d == 0 && at.piece == 0) store_factors(at, r, mul + (n & 1) * 128);
         uint8_t *dst = smem + PX_K + d * 2 * 16384;
@@ -647,7 +651,6 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
         if (lane == 0) mbar_arrive(&full[d]);
         x = ahead;
       }
-      seen = n - 1;
     }
   } else if (warp >= PX_ISSUE_WARP) {
     regs_down<PX_REG_ISSUE>();
@@ -656,13 +659,16 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
       const uint32_t kt = smem_u32(smem + PX_K);
       if (p.shared > 0) asm volatile("fence.proxy.async;" ::: "memory");  // (the expansion's stores were generic ones)
       bool ok = true;
-      int last[4] = {-1, -1, -1, -1}, never = 0, seen = -1;
+      int last[4] = {-1, -1, -1, -1}, never = 0;
       auto wait = [&](int d, int n) {
         return __all_sync(0xffffffffu, mbar_wait_bounded(&freed[d], n & 1, abort_flag, PX_WAIT_NS));
       };
       for (int n = 0; w.left > 0 && ok; ++n, w.next(p)) {
-        if (!w.within(limit)) continue;
-        for (; ok && seen < n - 2; ++seen) ok = wait(3, seen + 1);  // (as the producers)
+        if (!w.within(limit)) {  // the producers' tile (see there)
+          if (n > 0) ok = wait(0, n - 1);
+          if (lane == 0) mbar_arrive(&full[0]);
+          continue;
+        }
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           if (ok && n > 0) ok = wait(d, n - 1);
@@ -671,12 +677,11 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
             mbar_arrive_expect_tx(&full[d], 2 * 16384);
             tma_block(kt + (2 * d) * 16384, &map, 2 * d, w.tile, &full[d]);
             tma_block(kt + (2 * d + 1) * 16384, &map, 2 * d + 1, w.tile, &full[d]);
-          } else if (ok && lane < 8) {
+          } else if (ok && d > 0 && lane < 8) {
             mbar_arrive(&full[d]);  // (the barrier counts the eight producer warps)
           }
           __syncwarp();
         }
-        seen = n - 1;
       }
       if (!ok)  // given up: the copies under way still have to land before the block ends
         for (int d = 0; d < 4; ++d)
