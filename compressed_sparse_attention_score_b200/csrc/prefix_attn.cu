@@ -474,8 +474,9 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + PX_BAR);  // [4] pair of blocks written
   uint64_t *freed = full + 4;                                    // [4] pair of blocks consumed
   uint64_t *s_full = freed + 4, *o_full = s_full + 1, *p_full = s_full + 2, *q_full = s_full + 3, *idle = s_full + 4;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 5);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(s_full + 6), *moving = abort_flag + 1;
+  uint64_t *p_again = s_full + 5;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_full + 6);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(s_full + 7), *moving = abort_flag + 1;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (p.shared == 0) grid_dep_wait();  // (the inputs may be the previous kernel's work)
@@ -597,6 +598,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
     mbar_init(s_full, 1);
     mbar_init(o_full, 1);
     mbar_init(p_full, 8);
+    mbar_init(p_again, 8);
     mbar_init(q_full, 8);
     mbar_init(idle, 1);
     *abort_flag = 0;
@@ -719,7 +721,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
         commit_to(leader, &freed[d]);
       };
       bool begins = true, more = true;
-      for (int n = 0, piece = 0, written = 0; more; ++n) {
+      for (int n = 0, piece = 0, moved = 0; more; ++n) {
         if (begins) {  // S^T of a piece's first tile
           if (!wait(q_full, piece)) break;
           if (!step_s(n, 0, true) || !step_s(n, 1, false) || !step_s(n, 2, false) || !step_s(n, 3, false)) break;
@@ -727,10 +729,11 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
         }
         const bool ends = w.ends_piece();
         // P^T counts once all warps have written it, unless one of them has found that a reference has to move: then once
-        // they have all written it again
-        if (!wait(p_full, written++)) break;
+        // they have all written it again (which has a barrier of its own: on one, the second writing could end before this
+        // warp has seen the first, and parity would not tell)
+        if (!wait(p_full, n)) break;
         if (*moving) {
-          if (!wait(p_full, written++)) break;
+          if (!wait(p_again, moved++)) break;
           *moving = 0;
           __syncwarp();
         }
@@ -829,9 +832,10 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
         if (round > 0) {
           const float top = weights();
           const bool moves = __any_sync(0xffffffffu, round == 1 && top > PX_LAG + PX_BIAS);
+          __syncwarp();  // (the lanes' parts of P^T stand before the arrival)
           if (lane == 0) {  // (the vote below is off the tensor core's path)
             if (moves) *moving = 1;
-            mbar_arrive(p_full);
+            mbar_arrive(begins || round == 1 ? p_full : p_again);
           }
           if (!soft_any(!ok || moves)) break;
         }

@@ -1,9 +1,10 @@
 """csa2_prefix_attn where its warps hand tiles to one another."""
+import numpy as np
 import pytest
 import torch
 
-from tests.helpers import K, to_np
-from tests.test_gpu_prefix import DEV, Batch, check, everything
+from tests.helpers import ATOL_MAX, K, to_np
+from tests.test_gpu_prefix import DEV, TAU, Batch, check, everything, make
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +37,34 @@ def test_tiles_change_hands_under_memory_traffic():
         assert k.csa2_check(t.err) == 0
         for o2, lse2 in outs:
             assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def rising(t, heads):
+    """The given heads' logits rise along the keys by 8 bits a tile (the lag is 5), up to 4 tau |q|: a reference moves in
+    all but a few of the tiles."""
+    up = torch.nn.functional.normalize(torch.randn(512, generator=torch.Generator().manual_seed(5)), dim=0).to(DEV)
+    n = t.S
+    rise = torch.arange(n, device=DEV)[:, None] / n * 4.0
+    t.prefix = t._pack(0, 0, make((n, 512), 6) * 0.05 + up * rise)
+    top = 8 * 0.6931 * n / 128  # in natural units
+    t.q[:, :, heads] = (up * (top / 4.0 / TAU)).to(torch.bfloat16)
+    return top
+
+
+@pytest.mark.parametrize("S,tails,window,Q", [(2000, [3, 200], 128, 1), (3000, [0, 9, 300, 1, 70], 100, 5)])
+def test_references_move_in_every_tile(S, tails, window, Q):
+    """Weights written twice in tile after tile, in one head and in all, beside heads whose references stay; the same bits
+    every time.  A logit is a sum of 32 products of the tensor core, each sum off by 2^-23 of its size at most: 2^-18 of the
+    largest logit, which a weight and lse are off by too, and an output by twice that times the largest value."""
+    for heads in (slice(5, 6), slice(0, 64)):
+        t = Batch(S, tails, 1, 16, window, Q, seed=44)
+        off = rising(t, heads) * 2.0 ** -18
+        wo, wl = (to_np(x) for x in everything(t))
+        runs = [t.run() for _ in range(10)]
+        assert K().csa2_check(t.err) == 0
+        o, lse = (to_np(x).astype(np.float64) for x in runs[0])
+        size = max(np.abs(t.prefix).max(), 4.0)
+        assert np.abs(lse - wl).max() <= 1e-4 + off
+        assert np.abs(o - wo).max() <= ATOL_MAX * size / 4 + 2 * off * size
+        for o, lse in runs[1:]:
+            assert torch.equal(o, runs[0][0]) and torch.equal(lse, runs[0][1])
