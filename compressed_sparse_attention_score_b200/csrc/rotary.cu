@@ -186,7 +186,7 @@ void launch(const RotateArgs &a, int tokens, cudaStream_t st) {
   const bool words = ((a.dim | a.rot.first | a.rot.rot_dim) & 7) == 0 && (!half || (a.rot.rot_dim & 15) == 0) &&
                      (strides & 7) == 0 && ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out)) & 15) == 0;
   int hpb = a.heads;  // heads per block: all, or fewer while the blocks would not fill the device
-  while (int64_t(hpb) * units > 256 && int64_t(tokens) * ((a.heads + hpb - 1) / hpb) < 16 * sm_count()) hpb = (hpb + 1) / 2;
+  while (hpb > 1 && int64_t(hpb) * units > 256 && int64_t(tokens) * ((a.heads + hpb - 1) / hpb) < 16 * sm_count()) hpb = (hpb + 1) / 2;
   if (words && a.rot.rot_dim <= 4096 && int64_t(hpb) * units * units < (int64_t(1) << 32) && (a.heads + hpb - 1) / hpb <= 65535) {
     // u / units as a multiplication, exact for u units < 2^32 (one unit a head: no division)
     const uint32_t magic = units == 1 ? 0u : uint32_t(((uint64_t(1) << 32) + units - 1) / units);
