@@ -1017,7 +1017,7 @@ __global__ void __launch_bounds__(256) prefix_combine_kernel(const __grid_consta
         if (i0 + lane < n) m = part(i0 + lane)[PX_PART + h], l = part(i0 + lane)[PX_PART + H + h];
       }
       w = m == -INFINITY ? 0.f : ex2(m - M);
-      l = w == 0.f ? 0.f : w * l;
+      l = l == 0.f ? 0.f : w * l;  // (a sum that is NaN stays, also under a reference of -inf: all its logits are NaN)
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -68,3 +68,18 @@ def test_references_move_in_every_tile(S, tails, window, Q):
         assert np.abs(o - wo).max() <= ATOL_MAX * size / 4 + 2 * off * size
         for o, lse in runs[1:]:
             assert torch.equal(o, runs[0][0]) and torch.equal(lse, runs[0][1])
+
+
+@pytest.mark.parametrize("S,B,Q", [(50, 3, 1), (300, 3, 1), (2500, 3, 1), (12800, 4, 1), (140, 70, 6)])
+def test_heads_that_are_not_finite_are_nan(S, B, Q):
+    """A NaN or an infinity in a query head makes its output and its lse NaN, whether its row lies in one block or in
+    several (an lse of -inf would say that it sees no key)."""
+    t = Batch(S, [3] * B, 1, 16, 128, Q, seed=45)
+    t.q[0, 0, 7, 100], t.q[1, 0, 0, 0], t.q[2, 0, 63, 511] = float("inf"), float("nan"), -float("inf")
+    t.q[1, 0, 20] = float("nan")
+    o, lse = t.run()
+    assert K().csa2_check(t.err) == 0
+    bad = torch.zeros((B, Q, 64), dtype=torch.bool, device=DEV)
+    bad[0, 0, 7] = bad[1, 0, 0] = bad[1, 0, 20] = bad[2, 0, 63] = True
+    assert torch.isnan(lse[bad]).all() and torch.isnan(o[bad]).all()
+    assert torch.isfinite(lse[~bad]).all() and torch.isfinite(o[~bad]).all()
