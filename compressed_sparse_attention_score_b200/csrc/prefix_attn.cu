@@ -279,7 +279,7 @@ __device__ __forceinline__ void load_keys(const PrefixArgs &p, const KeyPlace &a
   }
 }
 
-// The factors of the logits and weights of the tile's keys (NaN: no key).
+// The factors of the logits and weights of the tile's keys (NaN and 0: no key; a window token's scale may be NaN itself, in both).
 __device__ __forceinline__ void store_factors(const KeyPlace &at, const KeyPart &r, float2 *mul) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(PX_THREADS, 1) prefix_attn_kernel(const __grid
       __syncwarp();
       const bool shared = w.within(limit);
       const float2 m2 = shared ? make_float2(1.f, 1.f) : mul[(n & 1) * 128 + key];
-      const bool valid = m2.x == m2.x;
+      const bool valid = m2.x == m2.x || m2.y != 0.f;
       const bool plain = shared || __all_sync(0xffffffffu, m2.x == 1.f);  // this warp's keys are all entries
       float s[32];
       // The weights 2^(logit - reference + BIAS) into s and, times the keys' factors, in fp16 into P^T;

@@ -83,3 +83,27 @@ def test_heads_that_are_not_finite_are_nan(S, B, Q):
     bad[0, 0, 7] = bad[1, 0, 0] = bad[1, 0, 20] = bad[2, 0, 63] = True
     assert torch.isnan(lse[bad]).all() and torch.isnan(o[bad]).all()
     assert torch.isfinite(lse[~bad]).all() and torch.isfinite(o[~bad]).all()
+
+
+@pytest.mark.parametrize("S,B", [(30, 3), (150, 3), (12800, 4)])
+def test_a_window_scale_that_is_nan_is_seen(S, B):
+    """A window token whose scale is NaN makes every head of the queries that see it NaN, as csa2_sparse_attn does; the
+    other sequences, and one whose ring holds it outside the window, are as before (of 33 entries position -18's slot is
+    outside it for both)."""
+    k = K()
+    t = Batch(S, [3] * B, 1, 16, 100, 1, seed=46)
+    wo, wl = (to_np(x) for x in everything(t))
+    ring = t.ring
+    t.scale[1, (int(t.q_pos[1, 0]) - 50) % ring] = float("nan")
+    t.scale[2, (int(t.q_pos[2, 0]) - 100) % ring] = float("nan")  # one position too old
+    o, lse = t.run()
+    assert k.csa2_check(t.err) == 0
+    inside = int(t.q_pos[1, 0]) >= 50
+    assert inside == (S > 30)
+    if inside:
+        assert torch.isnan(o[1]).all() and torch.isnan(lse[1]).all()
+    for b in (0, 2) if inside else (0, 1, 2):
+        check(o[b], lse[b], (wo[b], wl[b]), f"b={b}")
+    od, _ = k.csa2_sparse_attn("reuse", t.q, t.q_pos, t.cache, TAU, t.most, idx_in=torch.zeros((B, 1, 1), dtype=torch.int32, device=DEV),
+                                k=1, swa_codes=t.codes, swa_scale=t.scale, window=100)
+    assert torch.isnan(od[1]).all() == inside and torch.isfinite(od[0]).all()
