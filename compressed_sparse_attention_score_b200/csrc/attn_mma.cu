@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1) attn_mma_kernel(AttnArgs p) {
           if (n < -1 || n >= nvis) {
             report(p.err, CSA2_ERR_INDEX);
           } else {
-            sl[r] = cache_slot(p.c, b, n);
+            sl[r] = cache_slot<true>(p.c, b, n);
             if (sl[r] < 0) report(p.err, CSA2_ERR_INDEX);
           }
         }
@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(AM_THREADS, 1) attn_tile_kernel(AttnArgs p) {
         if (n < -1 || n >= nvis) {
           if (half == 0) report(p.err, CSA2_ERR_INDEX);
         } else {
-          s = cache_slot(p.c, b, n);
+          s = cache_slot<true>(p.c, b, n);
           if (s < 0 && half == 0) report(p.err, CSA2_ERR_INDEX);
         }
       }
@@ -1064,7 +1064,7 @@ void launch_attn_mma(const uint16_t *q, int B, int Q, const int32_t *q_pos, floa
   a.q = q, a.Q = Q, a.q_pos = q_pos, a.tau = tau;
   a.idx = dense ? nullptr : idx, a.k = (idx && !dense) ? k : 0;
   a.dense = dense ? 1 : 0, a.e0 = e0, a.e1 = e1, a.n_bound = n_bound;
-  if (c) a.c = *c;
+  if (c) a.c = divisible_pages(*c);
   a.codes = codes, a.scale = scale, a.R = R, a.window = window, a.swa_new = codes ? swa_new : nullptr;
   a.o = o, a.lse = lse, a.err = err;
   const int nkeys = (dense ? max(0, e1 - e0) : a.k) + (codes ? window : 0);

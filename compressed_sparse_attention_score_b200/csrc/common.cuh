@@ -79,14 +79,24 @@ __device__ __forceinline__ float pow2f(int e) {  // exact 2^e for e in [-127, 12
 }
 
 // ------------------------------------------------------------------ cache addressing
-// Physical slot of entry n of sequence b, or -1 if outside the cache.
+// Physical slot of entry n of sequence b, or -1 if outside the cache.  ANY: page_size need not be a power of two (the
+// plain append and the decode step take any; every other entry point refuses one that is not): the descriptor is one of
+// divisible_pages(), and the page is found by a multiplication (n < 2^31).  With a division in a branch of its own
+// instead, which no call of the bench takes, its step was 0.7 % slower.
+template <bool ANY>
 __device__ __forceinline__ int64_t cache_slot(const csa2_cache &c, int b, int64_t n) {
   int64_t s;
   if (c.page_table == nullptr) {
     if (n < 0 || n >= c.seq_stride) return -1;
     s = int64_t(b) * c.seq_stride + n;
+  } else if (ANY) {
+    const uint32_t p = __umulhi(2u * uint32_t(n), uint32_t(c.seq_stride)) >> (32 - __clz(c.page_size - 1));
+    if (n < 0 || p >= uint32_t(c.max_pages)) return -1;
+    const int32_t pid = c.page_table[int64_t(b) * c.max_pages + p];
+    if (pid < 0) return -1;
+    s = int64_t(pid) * c.page_size + (uint32_t(n) - p * uint32_t(c.page_size));
   } else {
-    const int shift = 31 - __clz(c.page_size);  // page_size is a power of two: no 64-bit divisions
+    const int shift = 31 - __clz(c.page_size);  // no 64-bit divisions
     int64_t p = n >> shift;
     if (n < 0 || p >= c.max_pages) return -1;
     int32_t pid = c.page_table[int64_t(b) * c.max_pages + p];

@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(IM_THREADS, 2) index_score_mma_kernel(const __
       if (a.cand && (n < -1 || n >= n_entries)) report(a.err, CSA2_ERR_INDEX);
       int64_t sv = -1;
       if (n >= 0 && n < nvis) {
-        sv = cache_slot(a.c, b, n);
+        sv = cache_slot<true>(a.c, b, n);
         if (sv < 0) report(a.err, CSA2_ERR_INDEX);
       }
       sl[j] = sv;
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(IM_THREADS, 2) index_score_mma_kernel(const __
   auto issue_tma = [&](int i) {  // one lane: tile i of a whole-group run (its stage is free)
     const int s = i % IM_STAGES;
     const uint32_t st = stages + s * IM_STAGE_BYTES;
-    const int64_t slot0 = cache_slot(a.c, b, int64_t(t0 + i) * IM_TILE);
+    const int64_t slot0 = cache_slot<true>(a.c, b, int64_t(t0 + i) * IM_TILE);
     if (slot0 >= 0 && (slot0 & (IM_TILE - 1)) == 0 && slot0 + IM_TILE <= a.c.num_slots) {
       mbar_arrive_expect_tx(&full[s], IM_A_BYTES + 512);
       tma_load_4d(st, &tmap, 0, 0, 0, int(slot0 / IM_TILE), &full[s]);
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(IM_THREADS, 2) index_score_mma_kernel(const __
       const float sc = weighted_relu_score(r0, r1, w4);
       const int pos = (t0 + i) * IM_TILE + e;
       if (pos < a.n_out) {
-        const bool ok = n_cur >= 0 && n_cur < nvis && cache_slot(a.c, b, n_cur) >= 0;
+        const bool ok = n_cur >= 0 && n_cur < nvis && cache_slot<true>(a.c, b, n_cur) >= 0;
         if constexpr (SEL)
           keys_l[pos - t0 * IM_TILE] = score_key(ok ? sc : -INFINITY);
         else
@@ -730,7 +730,7 @@ void launch_index_score_mma(const uint16_t *q_ix, const uint16_t *w, int B, int 
   CUtensorMap tmap;
   memset(&tmap, 0, sizeof(tmap));
   const bool use_tma = cand == nullptr && make_index_code_map(&tmap, c);
-  IndexMmaArgs a{use_tma, q_ix, w, Q, q_pos, cand, P, n_out, c, scores, err, chunk};
+  IndexMmaArgs a{use_tma, q_ix, w, Q, q_pos, cand, P, n_out, divisible_pages(c), scores, err, chunk};
   a.rows = rows;
   set_smem_limit(index_score_mma_kernel<false>, IM_SMEM_BYTES);
   // A full scan of 2 to 32 rows deals the CTAs to the rows by their visible entries (a ragged
@@ -807,7 +807,7 @@ void launch_reindex_select(const uint16_t *q_ix, const uint16_t *w, int B, int Q
   const int chunk = (t_all + cs - 1) / cs;
   CUtensorMap tmap;
   memset(&tmap, 0, sizeof(tmap));
-  IndexMmaArgs a{false, q_ix, w, Q, q_pos, cand, P, P, c, nullptr, err, chunk, k, sel};
+  IndexMmaArgs a{false, q_ix, w, Q, q_pos, cand, P, P, divisible_pages(c), nullptr, err, chunk, k, sel};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cs, rows);
   cfg.blockDim = dim3(IM_THREADS);

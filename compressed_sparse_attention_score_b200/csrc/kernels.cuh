@@ -19,6 +19,18 @@ inline void set_smem_limit(F *func, size_t bytes) {
   done[dev] = true;
 }
 
+// The descriptor that cache_slot<true> takes: in a paged one seq_stride, which pages do not use, holds
+// ceil(2^(31 + l) / page_size) for l = ceil(log2 page_size), so that n / page_size is the high word of n times it, over 2^31,
+// shifted by l: exact for n < 2^31 (Granlund and Montgomery, "Division by invariant integers using multiplication", 1994).
+inline csa2_cache divisible_pages(csa2_cache c) {
+  if (c.page_table && c.page_size > 0) {
+    int l = 0;
+    while ((int64_t(1) << l) < c.page_size) ++l;
+    c.seq_stride = int32_t(uint32_t(((uint64_t(1) << (31 + l)) + c.page_size - 1) / c.page_size));
+  }
+  return c;
+}
+
 // Streaming multiprocessors of the current device (queried once per device).
 inline int sm_count() {
   static int cached[64] = {};

@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_
   const int64_t e = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (e >= int64_t(B) * n_new) return;
   const int b = int(e / n_new), j = int(e % n_new);
-  const int64_t n = int64_t(first_entry[b]) + j, slot = cache_slot(c, b, n);
+  const int64_t n = int64_t(first_entry[b]) + j, slot = cache_slot<false>(c, b, n);
   if (slot < 0) {
     if (lane == 0) report(err, CSA2_ERR_INDEX);
     return;
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(32 * PACK_WARPS<T>, PACK_BLOCKS<T>)
   int64_t first = first_entry[b];
   bool fresh = true;
   for (; left > 0; --left, ++e) {
-    const int64_t n = first + j, slot = cache_slot(c, b, n);
+    const int64_t n = first + j, slot = cache_slot<false>(c, b, n);
     float x[16], xi[4];
     raw_values(raw, x, xi);
     if (!one) {
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(256) append_kv_kernel(const T *__restrict__ la
   }
   if (cur != r - 1) return;  // the group is not complete yet
   const int j = p / r;
-  const int64_t slot = cache_slot(c, b, j);
+  const int64_t slot = cache_slot<!ROT>(c, b, j);
   if (slot < 0) {
     if (lane == 0) report(err, CSA2_ERR_INDEX);
     return;
@@ -717,7 +717,7 @@ static void append_kv(const void *lat_kv, const void *lat_ix, int B, const int32
                       int32_t *err, cudaStream_t st) {
   if (B == 0) return;
   append_kv_kernel<T, ROT><<<(B + 7) / 8, 256, 0, st>>>(static_cast<const T *>(lat_kv), static_cast<const T *>(lat_ix),
-                                                        B, pos, stage, stage_stride, c, num_entries, rw, err);
+                                                        B, pos, stage, stage_stride, ROT ? c : divisible_pages(c), num_entries, rw, err);
 }
 
 void launch_append_kv(const void *lat_kv, const void *lat_ix, csa2_dtype dtype, int B, const int32_t *pos,

@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(PF_THREADS, 2) prefill_index_kernel(const __gr
           const int s = i % PF_STAGES;
           if (!mbar_wait_bounded(&empty[s], ((i / PF_STAGES) & 1) ^ 1, abort_flag, PF_WAIT_NS)) break;
           const uint32_t st = stages + s * PF_STAGE_BYTES;
-          const int64_t slot0 = cache_slot(a.c, b, int64_t(i) * PF_TILE);
+          const int64_t slot0 = cache_slot<false>(a.c, b, int64_t(i) * PF_TILE);
           if (slot0 >= 0 && (slot0 & (PF_TILE - 1)) == 0 && slot0 + PF_TILE <= a.c.num_slots) {
             mbar_arrive_expect_tx(&full[s], PF_A_BYTES + 512);
             tma_load_4d(st, &tmap, 0, 0, 0, int(slot0 / PF_TILE), &full[s]);
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(PF_THREADS, 2) prefill_index_kernel(const __gr
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int e = lane + 32 * j, n = i * PF_TILE + e, m = pf_row_of_entry(e);
-          const int64_t slot = n < nvis_max ? cache_slot(a.c, b, n) : -1;
+          const int64_t slot = n < nvis_max ? cache_slot<false>(a.c, b, n) : -1;
           if (slot >= 0) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(PF_THREADS, 2) prefill_index_kernel(const __gr
       // candidate (its error is already reported)
       const int n = i * PF_TILE + e;
       const uint32_t key = score_key(sc);
-      const bool pass = ok && n < qv && key > thr && cache_slot(a.c, b, n) >= 0;
+      const bool pass = ok && n < qv && key > thr && cache_slot<false>(a.c, b, n) >= 0;
       const uint32_t m = __ballot_sync(0xffffffffu, pass);
       if (m) {
         uint32_t base = 0;
