@@ -244,6 +244,7 @@ __device__ __forceinline__ void store_entry(const float (&x)[16], const float (&
 struct RotaryWrite {
   csa2_rotary kv, ix;  // rot_dim 0: not turned
   bool same;           // both use one table and turn as many dims: one sine and cosine serve both
+  bool runs;           // at most 32 pairs of one table: pack_run_kernel's entries, whose angles are formed in groups
   uint16_t *kv_hat, *ix_hat;
 };
 
@@ -254,9 +255,9 @@ constexpr int TURN_MAIN = D + 4 * (D / 16), TURN_ROW = TURN_MAIN + DI;
 
 // Pair (a, b) turned in fp64 and rounded once to fp32.
 __device__ __forceinline__ void turn_pair(float &a, float &b, double2 cs, float scale) {
-  const double x = a, y = b, g = scale;
-  a = float((x * cs.x - y * cs.y) * g);
-  b = float((x * cs.y + y * cs.x) * g);
+  const double2 v = turned_by(make_double2(a, b), cs);
+  a = float(__dmul_rn(v.x, scale));
+  b = float(__dmul_rn(v.y, scale));
 }
 
 // Turn the values a warp holds (x: main, lane l 16l ..; xi: indexer, lane l 4l .., or none) through the warp's row `buf` of
@@ -294,11 +295,21 @@ __device__ __forceinline__ void turn_index(const csa2_rotary &ix, int i, double2
   turn_pair(buf[TURN_MAIN + rotary_dim0(ix, i)], buf[TURN_MAIN + rotary_dim1(ix, i)], cs, ix.scale);
 }
 
-// At position pos, one pair per lane and step.
+// At position pos, one pair per lane and step.  `runs`: entry n of a cache of ratio r, with the angles of pack_run_kernel.
 template <bool IX>
 __device__ __forceinline__ void turn_values(float (&x)[16], float (&xi)[4], const csa2_rotary &kv, const csa2_rotary &ix,
-                                            bool same, int64_t pos, float *buf, int lane) {
+                                            bool same, int64_t pos, float *buf, int lane, bool runs = false, int64_t n = 0,
+                                            int r = 1) {
   turn_through<IX>(x, xi, kv.rot_dim != 0, ix.rot_dim != 0, buf, lane, [&]() {
+    if (IX && runs) {
+      if (lane >= max(kv.rot_dim, ix.rot_dim) / 2) return;
+      const uint64_t step = (kv.rot_dim ? kv.step : ix.step)[lane];
+      EntryAngle angle(step, r);
+      angle.start(n);
+      if (kv.rot_dim) turn_main(kv, lane, angle.at, buf);
+      if (ix.rot_dim) turn_index(ix, lane, angle.at, buf);
+      return;
+    }
     for (int i = lane; i < kv.rot_dim / 2; i += 32) {
       const double2 cs = rotary_cs64(kv.step[i], pos);
       turn_main(kv, i, cs, buf);
@@ -308,16 +319,6 @@ __device__ __forceinline__ void turn_values(float (&x)[16], float (&xi)[4], cons
       for (int i = lane; i < ix.rot_dim / 2; i += 32) turn_index(ix, i, rotary_cs64(ix.step[i], pos), buf);
   });
 }
-
-// cos and sin of a pair at a position that goes up in equal steps: each is the last one turned by a step's angle (an error of
-// 2^-53 a step; a new start after at most 64).
-struct Turning {
-  double2 at, by;
-  __device__ __forceinline__ void start(uint64_t step, int64_t pos) { at = rotary_cs64(step, pos); }
-  __device__ __forceinline__ void next() {
-    at = make_double2(at.x * by.x - at.y * by.y, at.x * by.y + at.y * by.x);
-  }
-};
 
 // exp(x) from a fixed sequence of fp32 operations (so that the gated compressor's weights,
 // and through them the quantised codes, do not depend on a math library): t = x log2(e),
@@ -438,8 +439,8 @@ __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_
 }
 
 // The rotating pack of a chunk whose main and indexer values share one table of at most 32 pairs: a warp takes `run`
-// consecutive entries (lanes as in pack_kv_kernel; lane l turns pair l), so that a sine and cosine in fp64 serve a run, and asks
-// for the next entry's first token before it quantises this one.  Bound by instruction issue (about 440 a warp and
+// consecutive entries (lanes as in pack_kv_kernel; lane l turns pair l), so that a sine and cosine in fp64 serve 32 of them
+// (EntryAngle), and asks for the next entry's first token before it quantises this one.  Bound by instruction issue (about 440 a warp and
 // entry) and what of its latencies 24 warps an SM leave: 131288 bf16 tokens, r = 1, with the values stored, 82 us (71 % of
 // the copy rate; a sine and cosine per entry 162 us); 64000 fp32 tokens 49 us.  Blocks are as many as leave
 // registers enough: with 64 a thread, 32 warps an SM, a few spilled values made it 99 us (fp32, 80 a thread: 65 us).
@@ -460,16 +461,15 @@ __global__ void __launch_bounds__(32 * PACK_WARPS<T>, PACK_BLOCKS<T>)
   int left = int(min(int64_t(run), all - e));
   if (left <= 0) return;
   int b = int(e / n_new), j = int(e % n_new);
-  Turning turning;
   const bool turns = lane < max(rw.kv.rot_dim, rw.ix.rot_dim) / 2;
   const uint64_t step = turns ? (rw.kv.rot_dim ? rw.kv.step : rw.ix.step)[lane] : 0;
-  turning.by = rotary_cs64(step, r);
   const bool one = r == 1 && !pool_w;  // the entry is its token
   const float w_default = __fdiv_rn(1.0f, float(r));
   Raw16<T> raw;
   auto load = [&](int64_t tok) { load_raw(lat_kv + tok * D + 16 * lane, lat_ix + tok * DI + 4 * lane, raw); };
   load(int64_t(b) * T_ + int64_t(j) * r);
   int64_t first = first_entry[b];
+  EntryAngle angle(step, r);
   bool fresh = true;
   for (; left > 0; --left, ++e) {
     const int64_t n = first + j, slot = cache_slot<false>(c, b, n);
@@ -494,8 +494,8 @@ __global__ void __launch_bounds__(32 * PACK_WARPS<T>, PACK_BLOCKS<T>)
       }
     }
     // this entry's angle; then on to the next one
-    if (fresh) turning.start(step, n * r);
-    else turning.next();
+    if (fresh) angle.start(n);
+    else angle.next(n);
     fresh = false;
     if (++j == n_new) {
       j = 0, ++b;
@@ -507,8 +507,8 @@ __global__ void __launch_bounds__(32 * PACK_WARPS<T>, PACK_BLOCKS<T>)
     }
     turn_through<true>(x, xi, rw.kv.rot_dim != 0, rw.ix.rot_dim != 0, buf, lane, [&]() {
       if (turns) {
-        if (rw.kv.rot_dim) turn_main(rw.kv, lane, turning.at, buf);
-        if (rw.ix.rot_dim) turn_index(rw.ix, lane, turning.at, buf);
+        if (rw.kv.rot_dim) turn_main(rw.kv, lane, angle.at, buf);
+        if (rw.ix.rot_dim) turn_index(rw.ix, lane, angle.at, buf);
       }
     });
     if (slot < 0) {
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(256) append_kv_kernel(const T *__restrict__ la
     for (int i = 0; i < 4; ++i) xi[i] = t == 0 ? __fmul_rn(wt, ui[i]) : __fadd_rn(xi[i], __fmul_rn(wt, ui[i]));
   }
   if constexpr (ROT) {
-    turn_values<true>(x, xi, rw.kv, rw.ix, rw.same, int64_t(j) * r, turn_buf[threadIdx.x >> 5], lane);
+    turn_values<true>(x, xi, rw.kv, rw.ix, rw.same, int64_t(j) * r, turn_buf[threadIdx.x >> 5], lane, rw.runs, j, r);
     store_entry(x, xi, slot, c, lane, rw.kv_hat ? rw.kv_hat + int64_t(b) * D : nullptr,
                 rw.ix_hat ? rw.ix_hat + int64_t(b) * DI : nullptr);
   } else {
@@ -650,6 +650,7 @@ static RotaryWrite rotary_write(const csa2_rotary *kv, const csa2_rotary *ix, ui
   if (kv) w.kv = *kv;
   if (ix) w.ix = *ix;
   w.same = kv && ix && kv->step == ix->step && kv->rot_dim == ix->rot_dim;
+  w.runs = (w.same || !w.kv.rot_dim || !w.ix.rot_dim) && w.kv.rot_dim <= 64 && w.ix.rot_dim <= 64;
   w.kv_hat = kv_hat, w.ix_hat = ix_hat;
   return w;
 }
@@ -660,7 +661,7 @@ static void pack_kv(const void *lat_kv, const void *lat_ix, const float *pool_w,
                     const RotaryWrite &rw, int32_t *err, cudaStream_t st) {
   const int64_t n = int64_t(B) * (T_ / c.ratio);
   if (n == 0) return;
-  if (ROT && !gate_kv && (rw.same || !rw.kv.rot_dim || !rw.ix.rot_dim) && rw.kv.rot_dim <= 64 && rw.ix.rot_dim <= 64) {
+  if (ROT && !gate_kv && rw.runs) {
     // runs of up to PACK_RUN entries, of a length that fills the device a whole number of times
     const int64_t fit = int64_t(sm_count()) * PACK_WARPS<T> * PACK_BLOCKS<T>;  // warps at once
     const int64_t rounds = (n + PACK_RUN * fit - 1) / (PACK_RUN * fit);

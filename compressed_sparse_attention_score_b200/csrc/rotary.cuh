@@ -24,6 +24,32 @@ __device__ __forceinline__ double2 rotary_cs64(uint64_t step, int64_t p) {
   return make_double2(c, s);
 }
 
+// (a.x + i a.y)(b.x + i b.y), each rounding named: the same bits in every kernel.
+__device__ __forceinline__ double2 turned_by(double2 a, double2 b) {
+  return make_double2(__fma_rn(a.x, b.x, -__dmul_rn(a.y, b.y)), __fma_rn(a.x, b.y, __dmul_rn(a.y, b.x)));
+}
+
+// cos and sin of entry n of a cache of ratio r (position n r): those of the first of its 32 entries, turned n % 32 times by one
+// entry's angle.  A run of entries has them from one to the next, and yet they are a function of n alone, wherever a chunk
+// begins or a warp's run does, and the same in the append.  The first and the angle are off by (pi + 2) 2^-53 at most (the turn
+// rounded, sincospi's two units in the last place), a product by three roundings more: 2^-44 in all.
+struct EntryAngle {
+  double2 at, by;
+  uint64_t step;
+  int r;
+  __device__ __forceinline__ EntryAngle(uint64_t step, int r) : by(rotary_cs64(step, r)), step(step), r(r) {}
+  __device__ __forceinline__ void first(int64_t n) { at = rotary_cs64(step, (n & ~int64_t(31)) * r); }
+  __device__ __forceinline__ void start(int64_t n) {
+    first(n);
+    for (int k = int(n & 31); k > 0; --k) at = turned_by(at, by);
+  }
+  // from entry n - 1 to n
+  __device__ __forceinline__ void next(int64_t n) {
+    if (n & 31) at = turned_by(at, by);
+    else first(n);
+  }
+};
+
 // Dims (from the head's start) of pair i.
 __device__ __forceinline__ int rotary_dim0(const csa2_rotary &r, int i) {
   return r.first + (r.layout == CSA2_ROTARY_HALF ? i : 2 * i);

@@ -486,8 +486,11 @@ csa2_status csa2_rotate(const void *x, csa2_dtype x_dtype, int64_t x_token_strid
  * csa2_pack_kv / csa2_pack_kv_gated with the rotation applied between pooling and quantisation:
  * entry n of a cache of ratio r is turned at position n r, that of its group's first token.
  *   rot_kv, rot_ix: rotations of the 512 main and the 128 indexer values (host structures; NULL:
- *   those values are not turned).  The pooled fp32 values are turned in fp64 and rounded once to
- *   fp32, so the codes do not depend on a math library; then quantised as csa2_pack_kv does.
+ *   those values are not turned).  The pooled fp32 values are turned in fp64, by angles that are
+ *   off by less than 2^-44, and rounded once to fp32 (another math library's sine changes one fp32
+ *   value in some 2^20, and hardly ever a code); then quantised as csa2_pack_kv does.  An entry's
+ *   angles follow from its number, the ratio and the rotations alone: its bytes are the same in a
+ *   chunk of any size and when csa2_append_kv_rotary completes it.
  *   pool_w as csa2_pack_kv, or gate_kv and gate_ix as csa2_pack_kv_gated (not both; all NULL: the mean).
  *   kv_hat [B][T/r][512], ix_hat [B][T/r][128] bf16 (optional, NULL: none) receive the values that
  *   the new entries' codes stand for, exactly (what attention will read back).

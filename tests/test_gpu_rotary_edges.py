@@ -4,8 +4,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import rotary as R
 from tests.helpers import K, to_np
-from tests.test_gpu_rotary import DEV, check_rotated, make, table
+from tests.test_gpu_rotary import DEV, check_rotated, make, planes_of, rot_args, table
 
 pytestmark = pytest.mark.gpu
 BOTH = (torch.float32, torch.bfloat16)
@@ -56,3 +57,98 @@ def test_rotate_blocks_of_several_trips(layout):
         k.csa2_rotate(y, pos, rotary, out=y)
         keep = pos >= 0
         assert torch.equal(y[keep], k.csa2_rotate(x, pos, rotary)[keep]) and torch.equal(y[7], x[7])
+
+
+# ------------------------------------------------------------------ runs of several entries
+def one_table(scale=1.125):
+    """Rotations of the main and the indexer values by one table, as the runs need it."""
+    step = table(64, scaling="yarn", factor=16.0, original_len=65536)[0].to(DEV)
+    return K().Rotary(step, 448, "interleaved", scale), K().Rotary(step, 32, "half", scale)
+
+
+def warps_at_once(dtype):
+    return torch.cuda.get_device_properties(0).multi_processor_count * (24 if dtype == torch.bfloat16 else 20)
+
+
+def room(B, ratio, entries, page, gap=None):
+    """A cache of `entries` entries a sequence in shuffled pages, filled with 0xA5; page `gap` (b, p) is left out."""
+    k = K()
+    n = -(-entries // page)
+    perm = torch.randperm(B * n, generator=torch.Generator().manual_seed(3)).view(B, n).to(torch.int32).to(DEV)
+    if gap:
+        perm[gap] = -1
+    c = k.GlobalKVCache(B, ratio, num_slots=B * n * page, page_table=perm, page_size=page)
+    for p in c.planes:
+        p.fill_(0xA5)
+    return c
+
+
+@pytest.mark.parametrize("dtype,ratio,B,times,more,weights,main_only", [
+    (torch.bfloat16, 1, 3, 1, 3, False, False), (torch.bfloat16, 2, 2, 3, 5, True, False), (torch.bfloat16, 1, 5, 17, 11, False, False),
+    (torch.bfloat16, 1, 3, 64, 4, False, False), (torch.float32, 1, 2, 1, 5, True, False), (torch.float32, 2, 3, 4, 6, False, False),
+    (torch.float32, 1, 4, 21, 9, False, False), (torch.bfloat16, 2, 2, 9, 7, False, True)])
+def test_pack_in_runs(dtype, ratio, B, times, more, weights, main_only):
+    """More entries than the device has warps at once, so that a warp takes a run of them: across the ends of sequences with
+    unequal first entries, around a page outside the cache.  Every byte is that of the same tokens in chunks of a few
+    hundred, where a warp takes one entry; and some of the oracle's."""
+    k = K()
+    fit = warps_at_once(dtype)
+    n = -(-(times * fit + more) // B)
+    assert n * B > times * fit
+    T = n * ratio + (ratio > 1)  # (a token that completes no entry)
+    kv, ix = make((B, T, 512), 41, dtype), make((B, T, 128), 42, dtype)
+    w = torch.rand((B, T), device=DEV) if weights else None
+    first = [(0, 1003, 17, 5)[b] if b < 4 else 31 for b in range(B)]
+    page = 64
+    rk, ri = one_table()
+    if main_only:
+        ri = None
+    hats = lambda: (torch.full((B, n, 512), 9.0, dtype=torch.bfloat16, device=DEV), torch.full((B, n, 128), 9.0, dtype=torch.bfloat16, device=DEV))  # noqa: E731
+    a, b_ = (room(B, ratio, max(first) + n, page, (1, (first[1] + n // 2) // page)) for _ in range(2))
+    (kh, ih), (kh2, ih2), err = hats(), hats(), torch.zeros(2, dtype=torch.int32, device=DEV)
+    fe = torch.tensor(first, dtype=torch.int32, device=DEV)
+    k.csa2_pack_kv_rotary(kv, ix, fe, a, rk, ri, pool_w=w, kv_hat=kh, ix_hat=ih, err=err[:1])
+    assert k.csa2_check(err[:1]) == 5
+    gone = [j for j in range(n) if (first[1] + j) // page == (first[1] + n // 2) // page]
+    assert (kh[1, gone] == 9).all() and (ih[1, gone] == 9).all() and len(gone) == page
+    chunk = 331
+    for b in range(B):
+        view = b_.seq_view(b)
+        for j in range(0, n, chunk):
+            m = min(chunk, n - j)
+            s = slice(j * ratio, (j + m) * ratio)
+            hk, hi = kh2[b, j:j + m][None], ih2[b, j:j + m][None]
+            k.csa2_pack_kv_rotary(kv[b:b + 1, s].contiguous(), ix[b:b + 1, s].contiguous(), fe[b:b + 1] + j, view, rk, ri,
+                                  pool_w=None if w is None else w[b:b + 1, s].contiguous(), kv_hat=hk, ix_hat=hi, err=err[1:])
+    assert torch.equal(kh, kh2) and torch.equal(ih, ih2)
+    for x, y in zip(a.planes, b_.planes):
+        assert torch.equal(x, y)
+    rng = np.random.default_rng(5)
+    for b in range(B):
+        for j in [0, n - 37] + list(rng.integers(0, n - 37, 2)):
+            j = int(j)
+            if b == 1 and set(range(j, j + 37)) & set(gone):
+                continue
+            s = slice(j * ratio, (j + 37) * ratio)
+            want = R.pack_entries(to_np(kv[b, s]), to_np(ix[b, s]), first[b] + j, ratio, rot_args(rk), rot_args(ri), None if w is None else to_np(w[b, s]))
+            for x, y in zip(planes_of(a, b, first[b] + j + np.arange(37))[0], want):
+                np.testing.assert_array_equal(x, y.reshape(x.shape))
+
+
+@pytest.mark.parametrize("dtype,ratio", [(torch.bfloat16, 1), (torch.bfloat16, 2), (torch.float32, 1)])
+def test_append_is_the_pack_in_runs(dtype, ratio):
+    """The same tokens appended one at a time and packed at once in runs of several entries: the same bytes."""
+    k = K()
+    B, n, first = 8, 1100, 5
+    assert B * n > 2 * warps_at_once(dtype)
+    kv, ix = make((B, n * ratio, 512), 51, dtype), make((B, n * ratio, 128), 52, dtype)
+    rk, ri = one_table()
+    a, b = room(B, ratio, first + n, 16), room(B, ratio, first + n, 16)
+    fe = torch.full((B,), first, dtype=torch.int32, device=DEV)
+    k.csa2_pack_kv_rotary(kv, ix, fe, a, rk, ri)
+    stage = torch.zeros((B, ratio, 640), device=DEV) if ratio > 1 else None
+    for t in range(n * ratio):
+        k.csa2_append_kv_rotary(kv[:, t].contiguous(), ix[:, t].contiguous(), fe * ratio + t, b, rk, ri, stage=stage)
+    assert (b.num_entries == first + n).all()
+    for x, y in zip(a.planes, b.planes):
+        assert torch.equal(x, y)
