@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_
                                                       const int32_t *__restrict__ first_entry,
                                                       csa2_cache c, RotaryWrite rw, int32_t *err) {
   const int lane = threadIdx.x & 31;
-  __shared__ float turn_buf[ROT ? 8 : 1][ROT ? TURN_ROW : 1];
+  __shared__ __align__(16) float turn_buf[ROT ? 8 : 1][ROT ? TURN_ROW : 1];
   const int n_new = T_ / c.ratio;
   const int64_t e = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (e >= int64_t(B) * n_new) return;
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(32 * PACK_WARPS<T>, PACK_BLOCKS<T>)
     pack_run_kernel(const T *__restrict__ lat_kv, const T *__restrict__ lat_ix, const float *__restrict__ pool_w, int T_,
                     int n_new, int64_t all, int run, const int32_t *__restrict__ first_entry, csa2_cache c, RotaryWrite rw,
                     int32_t *err) {
-  __shared__ float turn_buf[PACK_WARPS<T>][TURN_ROW];
+  __shared__ __align__(16) float turn_buf[PACK_WARPS<T>][TURN_ROW];
   const int lane = threadIdx.x & 31, r = c.ratio;
   float *buf = turn_buf[threadIdx.x >> 5];
   int64_t e = (int64_t(blockIdx.x) * PACK_WARPS<T> + (threadIdx.x >> 5)) * run;
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(256) append_kv_kernel(const T *__restrict__ la
                                                         int64_t stage_stride, csa2_cache c, int32_t *num_entries,
                                                         RotaryWrite rw, int32_t *err) {
   const int lane = threadIdx.x & 31;
-  __shared__ float turn_buf[ROT ? 8 : 1][ROT ? TURN_ROW : 1];
+  __shared__ __align__(16) float turn_buf[ROT ? 8 : 1][ROT ? TURN_ROW : 1];
   const int b = int(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (b >= B) return;
   const int p = pos[b];
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(256) pack_swa_kernel(const T *__restrict__ x, 
                                                        float *__restrict__ scale, int R, csa2_rotary rot,
                                                        int32_t *err) {
   const int lane = threadIdx.x & 31;
-  __shared__ float turn_buf[ROT ? 8 : 1][ROT ? TURN_MAIN : 1];
+  __shared__ __align__(16) float turn_buf[ROT ? 8 : 1][ROT ? TURN_MAIN : 1];
   const int64_t e = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (e >= int64_t(B) * T_) return;
   const int b = int(e / T_), t = int(e % T_);
