@@ -10,7 +10,7 @@ _NAMES = ("EXPORTED", "MODE", "GlobalKVCache", "csa2_cache", "csa2_check", "csa2
           "csa2_topk", "csa2_version", "csa2_workspace_size", "raw", "LIB_PATH", "csa2_append_kv", "csa2_plan_v41",
           "csa2_pack_kv_gated", "csa2_index_topk", "DecodeStep", "LAYER_SWA", "Rotary", "csa2_rotary",
           "csa2_rotary_table", "csa2_rotate", "csa2_pack_kv_rotary", "csa2_append_kv_rotary", "csa2_pack_swa_rotary",
-          "csa2_prefix_workspace_size", "csa2_prefix_attn")
+          "csa2_prefix_workspace_size", "csa2_prefix_workspace_bytes", "csa2_prefix_attn")
 
 
 def __getattr__(name):

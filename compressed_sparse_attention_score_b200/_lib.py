@@ -106,6 +106,7 @@ _SIGS = {
     "csa2_pack_swa_rotary": ([c_void_p, ctypes.c_int, c_int32, c_int32, c_void_p, _PR, c_void_p, c_void_p, c_int32,
                               c_void_p, c_void_p], ctypes.c_int),
     "csa2_prefix_workspace_size": ([c_int32, c_int32, c_int32], c_size_t),
+    "csa2_prefix_workspace_bytes": ([c_int32, c_int32, c_int32, c_int32], c_size_t),
     "csa2_prefix_attn": ([c_void_p, c_int32, c_int32, c_void_p, c_float, c_int32, c_int32, _P, c_void_p, c_void_p,
                           c_int32, c_int32, c_void_p, ctypes.c_int, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p],
                          ctypes.c_int),
@@ -566,7 +567,13 @@ def csa2_pack_swa_rotary(x, pos, swa_codes, swa_scale, rotary, err=None, stream=
 
 
 def csa2_prefix_workspace_size(B, Q, max_entries):
+    """Workspace bytes of csa2_prefix_attn that are enough for every prefix_entries."""
     return _lib.csa2_prefix_workspace_size(B, Q, max_entries)
+
+
+def csa2_prefix_workspace_bytes(B, Q, max_entries, prefix_entries):
+    """Workspace bytes of csa2_prefix_attn for this prefix (what the call makes itself without ws)."""
+    return _lib.csa2_prefix_workspace_bytes(B, Q, max_entries, prefix_entries)
 
 
 def csa2_prefix_attn(q, q_pos, cache, softmax_scale, max_entries, prefix_entries, swa_codes=None, swa_scale=None,
@@ -581,7 +588,7 @@ def csa2_prefix_attn(q, q_pos, cache, softmax_scale, max_entries, prefix_entries
     if lse is None:
         lse = _new((B, Q, HEADS), torch.float32, q.device, stream)
     if ws is None:
-        ws = _new(max(csa2_prefix_workspace_size(B, Q, max_entries), 1), torch.uint8, q.device, stream)
+        ws = _new(max(csa2_prefix_workspace_bytes(B, Q, max_entries, prefix_entries), 1), torch.uint8, q.device, stream)
     elif ws.get_device() != i:
         raise ValueError("ws must be on the device of the call's other tensors")
     R = 0 if swa_codes is None else swa_codes.shape[1]

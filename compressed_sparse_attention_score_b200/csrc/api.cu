@@ -428,7 +428,12 @@ CSA2_EXPORT csa2_status csa2_pack_swa_rotary(const void *x, csa2_dtype dtype, in
 // ---------------------------------------------------------------- attention over a shared prefix
 CSA2_EXPORT size_t csa2_prefix_workspace_size(int32_t B, int32_t Q, int32_t max_entries) {
   if (B <= 0 || Q <= 0 || max_entries < 0) return 0;
-  return csa2::prefix_workspace(int64_t(B) * Q, max_entries);
+  return csa2::prefix_workspace(int64_t(B) * Q, max_entries, max_entries);
+}
+
+CSA2_EXPORT size_t csa2_prefix_workspace_bytes(int32_t B, int32_t Q, int32_t max_entries, int32_t prefix_entries) {
+  if (B <= 0 || Q <= 0 || max_entries < 0 || prefix_entries < 0) return 0;
+  return csa2::prefix_workspace(int64_t(B) * Q, max_entries, prefix_entries);
 }
 
 CSA2_EXPORT csa2_status csa2_prefix_attn(const uint16_t *q, int32_t B, int32_t Q, const int32_t *q_pos,
@@ -451,7 +456,7 @@ CSA2_EXPORT csa2_status csa2_prefix_attn(const uint16_t *q, int32_t B, int32_t Q
   // (key tiles are counted in 32 bits)
   if (int64_t(B) * Q > 65535 * 16 || int64_t(B) * Q * ((int64_t(max_entries) + 255) / 128) > INT32_MAX / 2)
     return fail(CSA2_ERR_UNSUPPORTED, "too many query rows per call");
-  if (!ws || !aligned16(ws) || ws_bytes < csa2_prefix_workspace_size(B, Q, max_entries))
+  if (!ws || !aligned16(ws) || ws_bytes < csa2_prefix_workspace_bytes(B, Q, max_entries, prefix_entries))
     return fail(CSA2_ERR_INVALID_ARG, "workspace too small or misaligned");
   csa2::launch_prefix_attn(q, B, Q, q_pos, softmax_scale, prefix_entries, max_entries, *cache, swa_codes, swa_scale, R,
                            window, o, o_dtype == CSA2_BF16, lse, ws, err, stream);

@@ -103,8 +103,8 @@ void launch_attn_mma(const uint16_t *q, int B, int Q, const int32_t *q_pos, floa
                      const float *scale, int R, int window, float *o, float *lse, int32_t *err, cudaStream_t st,
                      const uint16_t *swa_new = nullptr, bool pdl = false);
 // Dense attention whose first `prefix` entries are sequence 0's for every sequence, with the window
-// (codes may be NULL); ws holds prefix_workspace(B * Q, max_entries) bytes.
-size_t prefix_workspace(int64_t rows, int max_entries);
+// (codes may be NULL); ws holds prefix_workspace(B * Q, max_entries, prefix) bytes.
+size_t prefix_workspace(int64_t rows, int max_entries, int prefix);
 void launch_prefix_attn(const uint16_t *q, int B, int Q, const int32_t *q_pos, float tau, int prefix, int max_entries,
                         const csa2_cache &c, const uint8_t *codes, const float *scale, int R, int window, void *o,
                         bool o_bf16, float *lse, void *ws, int32_t *err, cudaStream_t st);

@@ -1067,8 +1067,8 @@ struct Layout {
 };
 }  // namespace
 
-size_t prefix_workspace(int64_t rows, int max_entries) {
-  return Layout(rows, max_entries, prefix_blocks(rows, max_entries, PX_MAX_CTAS)).bytes;
+size_t prefix_workspace(int64_t rows, int max_entries, int prefix) {
+  return Layout(rows, prefix < max_entries ? prefix : max_entries, prefix_blocks(rows, max_entries, PX_MAX_CTAS)).bytes;
 }
 
 void launch_prefix_attn(const uint16_t *q, int B, int Q, const int32_t *q_pos, float tau, int prefix, int max_entries,

@@ -529,8 +529,11 @@ csa2_status csa2_pack_swa_rotary(const void *x, csa2_dtype dtype, int32_t B, int
  *   q [B][Q][64][512] bf16; o [B][Q][64][512] in o_dtype (F32 or BF16); lse [B][Q][64] fp32.
  *   max_entries bounds num_entries; visibility, window, empty rows and device errors as
  *   csa2_sparse_attn.
- * ws: csa2_prefix_workspace_size(B, Q, max_entries) bytes, 16-byte aligned, used by one call at a time.
+ * ws: csa2_prefix_workspace_bytes(B, Q, max_entries, prefix_entries) bytes, 16-byte aligned, used by one
+ * call at a time; csa2_prefix_workspace_size(B, Q, max_entries) is enough for every prefix (from 400 tiles
+ * of 128 entries over all rows on, a prefix takes 1 KB an entry).
  */
+size_t csa2_prefix_workspace_bytes(int32_t B, int32_t Q, int32_t max_entries, int32_t prefix_entries);
 size_t csa2_prefix_workspace_size(int32_t B, int32_t Q, int32_t max_entries);
 csa2_status csa2_prefix_attn(const uint16_t *q, int32_t B, int32_t Q, const int32_t *q_pos,
                              float softmax_scale, int32_t prefix_entries, int32_t max_entries,

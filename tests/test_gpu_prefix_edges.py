@@ -107,3 +107,18 @@ def test_a_window_scale_that_is_nan_is_seen(S, B):
     od, _ = k.csa2_sparse_attn("reuse", t.q, t.q_pos, t.cache, TAU, t.most, idx_in=torch.zeros((B, 1, 1), dtype=torch.int32, device=DEV),
                                 k=1, swa_codes=t.codes, swa_scale=t.scale, window=100)
     assert torch.isnan(od[1]).all() == inside and torch.isfinite(od[0]).all()
+
+
+@pytest.mark.parametrize("S,tails,Q", [(140, [11 * (b % 5) for b in range(70)], 6), (300, [3000] + [1] * 39, 1)])
+def test_workspace_of_the_prefix_alone(S, tails, Q):
+    """A workspace of the prefix's own size, between guards that stay as they are."""
+    k = K()
+    t = Batch(S, tails, 1, 16, 128, Q, seed=47)
+    n, guard = k.csa2_prefix_workspace_bytes(t.B, Q, t.most, S), 4096
+    assert n <= k.csa2_prefix_workspace_size(t.B, Q, t.most)
+    room = torch.full((n + 2 * guard,), 0xFF, dtype=torch.uint8, device=DEV)
+    o, lse = t.run(ws=room[guard:guard + n])
+    assert k.csa2_check(t.err) == 0 and (room[:guard] == 0xFF).all() and (room[guard + n:] == 0xFF).all()
+    check(o, lse, tuple(to_np(x) for x in everything(t)), f"prefix {S}")
+    with pytest.raises(RuntimeError, match="workspace"):
+        t.run(ws=room[guard:guard + n - 1])

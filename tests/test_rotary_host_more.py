@@ -49,3 +49,15 @@ def test_rotate_of_wide_heads_reaches_its_launch(pkg):
              (1, 3, 2057, 6), (1, 1, 1 << 20, 2), (2000, 64, 512, 64)]
     r = without_a_device(ROTATE % (sizes,))
     assert r.stdout.strip() == "done", r.stdout + r.stderr
+
+
+def test_workspace_goes_by_the_prefix(pkg):
+    """A prefix of none or of a few entries does not ask for room for every entry that a sequence may have, more entries
+    never ask for less, and the size without a prefix is enough for all of them."""
+    size, fit = pkg.csa2_prefix_workspace_size, pkg.csa2_prefix_workspace_bytes
+    assert fit(8, 1, 1 << 20, 0) == fit(8, 1, 1 << 20, 1000) < 64 << 20 < 1 << 30 < size(8, 1, 1 << 20)
+    assert fit(8, 1, 1 << 20, 1 << 19) - fit(8, 1, 1 << 20, 0) == pytest.approx(512 << 20, rel=1e-3)
+    for B, Q, most in ((1, 1, 64), (4, 1, 12800), (70, 6, 200), (32, 1, 8229), (3, 2, 1 << 20)):
+        sizes = [fit(B, Q, most, p) for p in (0, 1, 127, 128, 4000, most // 2, most, 2 * most, 2 ** 31 - 1)]
+        assert sizes[:4] == sorted(sizes[:4]) and max(sizes) == sizes[-1] == sizes[-3] == size(B, Q, most) and min(sizes) > 0
+    assert fit(0, 1, 64, 4) == fit(1, -1, 64, 4) == fit(1, 1, -1, 4) == fit(1, 1, 64, -1) == 0
