@@ -470,7 +470,7 @@ def _err(err, index):
 
 def _cache_on(cache, index):
     d = cache.desc()
-    for t in (cache.kv_codes, cache.num_entries, cache.page_table):
+    for t in (cache.kv_codes, cache.kv_scales, cache.ix_codes, cache.ix_scales, cache.num_entries, cache.page_table):
         if t is not None and t.get_device() != index:
             raise ValueError("the cache must be on the device of the call's other tensors")
     return ctypes.byref(d)

@@ -61,3 +61,22 @@ def test_workspace_goes_by_the_prefix(pkg):
         sizes = [fit(B, Q, most, p) for p in (0, 1, 127, 128, 4000, most // 2, most, 2 * most, 2 ** 31 - 1)]
         assert sizes[:4] == sorted(sizes[:4]) and max(sizes) == sizes[-1] == sizes[-3] == size(B, Q, most) and min(sizes) > 0
     assert fit(0, 1, 64, 4) == fit(1, -1, 64, 4) == fit(1, 1, -1, 4) == fit(1, 1, 64, -1) == 0
+
+
+@pytest.mark.parametrize("astray", ["kv_codes", "kv_scales", "ix_codes", "ix_scales", "num_entries", "page_table"])
+def test_every_tensor_of_a_cache_is_on_the_calls_device(pkg, astray):
+    from compressed_sparse_attention_score_b200 import _lib
+
+    class On:
+        def __init__(self, device):
+            self.get_device = lambda: device
+
+    class Cache:
+        kv_codes = kv_scales = ix_codes = ix_scales = num_entries = page_table = On(0)
+        desc = staticmethod(_lib.csa2_cache)
+
+    c = Cache()
+    _lib._cache_on(c, 0)
+    setattr(c, astray, On(1))
+    with pytest.raises(ValueError, match="device"):
+        _lib._cache_on(c, 0)
