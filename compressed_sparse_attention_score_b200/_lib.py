@@ -481,11 +481,14 @@ def csa2_rotate(x, pos, rotary, inverse=False, out=None, out_dtype=None, stream=
 
     The token dims of x may be strided as long as they form one stride; out (default: a new tensor of out_dtype or
     x's type) may be x itself.  Tokens at negative positions are padding: their rows of out are left as they are.
+    Without out the call is differentiable in x (the gradient is the other direction's rotation; 0 for padding).
     """
     shape = x.shape
     if len(shape) < 2:
         raise ValueError("x must have a heads and a dim axis")
     index, s = _on(x, stream)
+    if out is None and x.requires_grad and torch.is_grad_enabled():
+        return _Rotate.apply(x, pos, rotary.step, rotary, inverse, out_dtype, stream)
     if out is None:
         out = _new(shape, out_dtype or x.dtype, x.device, stream)
     elif out.shape != shape or out.get_device() != index:
@@ -498,6 +501,22 @@ def csa2_rotate(x, pos, rotary, inverse=False, out=None, out_dtype=None, stream=
     _ok(_lib.csa2_rotate(x.data_ptr(), xd, xt, xh, out.data_ptr(), od, ot, oh, pos.numel(), shape[-2], shape[-1], p,
                          _rot(rotary, index), 1 if inverse else 0, s), "csa2_rotate")
     return out
+
+
+class _Rotate(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, pos, step, rotary, inverse, out_dtype, stream):
+        ctx.save_for_backward(pos, step)  # (changed in place before the backward pass, they raise there)
+        ctx.rotary, ctx.inverse, ctx.like = rotary, inverse, (x.shape, x.dtype)
+        return csa2_rotate(x, pos, rotary, inverse, None, out_dtype, stream)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        shape, dtype = ctx.like
+        dx = torch.zeros(shape, dtype=dtype, device=grad.device)
+        csa2_rotate(grad.contiguous(), ctx.saved_tensors[0], ctx.rotary, not ctx.inverse, dx)
+        return dx, None, None, None, None, None, None
 
 
 def _head_strides(t, what):

@@ -152,3 +152,56 @@ def test_append_is_the_pack_in_runs(dtype, ratio):
     assert (b.num_entries == first + n).all()
     for x, y in zip(a.planes, b.planes):
         assert torch.equal(x, y)
+
+
+# ------------------------------------------------------------------ the gradient
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("xd,od", [(torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32)])
+def test_gradient_through_autograd(layout, xd, od):
+    """x from a wider tensor, in a scaled rotation; rows of padding tokens have no gradient."""
+    k = K()
+    T, H, D = 9, 3, 48
+    rotary = k.Rotary(table(16)[0].to(DEV), 8, layout, 1.5)
+    pos = torch.randint(0, 1 << 20, (T,), device=DEV, dtype=torch.int32)
+    pos[4] = -1
+    keep = pos >= 0
+    for inverse in (False, True):
+        wide = make((T, H * D + 8), 61, xd).requires_grad_()
+        y = k.csa2_rotate(wide[:, 8:].view(T, H, D), pos, rotary, inverse=inverse, out_dtype=od)
+        assert y.requires_grad and y.dtype == od
+        check_rotated(y.detach()[keep], wide.detach()[:, 8:].view(T, H, D)[keep], pos[keep], rotary, inverse)
+        dy = make((T, H, D), 62, od)
+        y.backward(dy)
+        got = wide.grad[:, 8:].view(T, H, D)
+        assert wide.grad.dtype == xd and (wide.grad[:, :8] == 0).all() and (got[4] == 0).all()
+        check_rotated(got[keep], dy[keep], pos[keep], rotary, not inverse)
+    x = make((T, H, D), 63, xd).requires_grad_()
+    k.csa2_rotate(x, pos, rotary, out_dtype=od)[keep].sum().backward()  # a gradient without memory of its own
+    check_rotated(x.grad[keep], torch.ones((T, H, D), dtype=od, device=DEV)[keep], pos[keep], rotary, True)
+    # a difference quotient of the (linear) operator is its derivative up to rounding
+    if xd == od == torch.float32:
+        dy = make((T, H, D), 64)
+        x.grad = None
+        k.csa2_rotate(x, pos, rotary).backward(dy)
+        for h, d in ((0, 8), (1, 15), (2, 23), (0, 3)):
+            e = torch.zeros_like(x)
+            e[:, h, d] = 0.5
+            with torch.no_grad():
+                df = k.csa2_rotate(x + e, pos, rotary).double() - k.csa2_rotate(x - e, pos, rotary).double()
+            np.testing.assert_allclose(to_np((df * dy.double())[keep].sum((-1, -2))), to_np(x.grad[keep][:, h, d]), atol=H * D * 2.0 ** -20 * 16)
+
+
+def test_where_no_gradient_is_asked_for():
+    """Without grad mode, into a given tensor and with a table or positions changed since: no graph, or an error."""
+    k = K()
+    rotary = k.Rotary(table(16)[0].to(DEV), 0, "half", 1.0)
+    pos = torch.arange(4, dtype=torch.int32, device=DEV)
+    x = make((4, 2, 16), 65).requires_grad_()
+    with torch.no_grad():
+        assert not k.csa2_rotate(x, pos, rotary).requires_grad
+    assert not k.csa2_rotate(x, pos, rotary, out=torch.zeros((4, 2, 16), device=DEV)).requires_grad
+    for changed in (pos, rotary.step):
+        y = k.csa2_rotate(x, pos, rotary)
+        changed.add_(1)
+        with pytest.raises(RuntimeError, match="modified"):
+            y.sum().backward()
