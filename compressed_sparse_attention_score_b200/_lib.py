@@ -477,7 +477,8 @@ def _cache_on(cache, index):
 
 
 def csa2_rotate(x, pos, rotary, inverse=False, out=None, out_dtype=None, stream=None):
-    """Rotary positions of x [..., heads, dim] at positions pos [...] (inverse: turned back).
+    """Rotary positions of x [..., heads, dim] at positions pos [...] (inverse: turned back, with the same scale; what was
+    scaled by rotary.scale = g is taken back with Rotary(rotary.step, rotary.first, rotary.layout, 1 / g)).
 
     The token dims of x may be strided as long as they form one stride; out (default: a new tensor of out_dtype or
     x's type) may be x itself.  Tokens at negative positions are padding: their rows of out are left as they are.

@@ -470,8 +470,10 @@ csa2_status csa2_rotary_table(int32_t rot_dim, double base, csa2_rotary_scaling 
  *   x [tokens][heads][dim] in x_dtype, out the same shape in out_dtype (F32 or BF16 each), both
  *   with unit stride along dim and the given strides (in elements) between tokens and heads;
  *   pos [tokens] positions, a negative one marks a padding token, whose out is left as it is.
- *   inverse != 0: the transposed rotation (sin negated) with the same scale, which is also the
- *   gradient of the forward call with respect to x.
+ *   inverse != 0: the transposed rotation (sin negated) with the same scale, which is the gradient
+ *   of the forward call with respect to x.  With scale 1 it also takes the rotation back.  A rotation
+ *   scaled by g (a YaRN table's) is taken back by the inverse with a csa2_rotary of the same table
+ *   and scale 1 / g: so are attention outputs whose keys-as-values were written with scale g.
  * Computed in fp32 and rounded once to out_dtype; dims that are not turned are copied.
  * out == x (same type and strides) works in place and touches only the turned dims; otherwise out
  * must not overlap x.  Any dim, head count and rotation; multiples of 8 with 16-byte aligned rows

@@ -205,3 +205,24 @@ def test_where_no_gradient_is_asked_for():
         changed.add_(1)
         with pytest.raises(RuntimeError, match="modified"):
             y.sum().backward()
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+def test_a_scaled_rotation_is_taken_back_by_the_reciprocal_scale(layout):
+    """The inverse keeps the scale, which makes it the gradient: after a rotation scaled by g it gives g^2 times the turned
+    dims.  The rotation by the same table and 1 / g takes it back: twice the tolerance of a rotation, and the rounding of
+    1 / g (below a third of it)."""
+    k = K()
+    g = 0.1 * np.log(16) + 1
+    a = k.Rotary(table(64)[0].to(DEV), 448, layout, g)
+    back = k.Rotary(a.step, 448, layout, 1 / a.scale)
+    x, pos = make((50, 64, 512), 66), torch.randint(0, 1 << 20, (50,), device=DEV, dtype=torch.int32)
+    y = k.csa2_rotate(x, pos, a)
+    i, j = R.pair_dims(32, 448, layout)
+    size = (x[..., i].abs() + x[..., j].abs()).repeat(1, 1, 2)
+    at = np.concatenate((i, j))
+    once = k.csa2_rotate(y, pos, back, inverse=True)
+    assert ((once - x)[..., at].abs() <= size * 2.0 ** -19).all() and torch.equal(once[..., :448], x[..., :448])
+    twice = k.csa2_rotate(y, pos, a, inverse=True)
+    assert ((twice / g ** 2 - x)[..., at].abs() <= size * 2.0 ** -19).all()
+    assert ((twice - x)[..., at].abs() > 0.5 * x[..., at].abs() - size * 2.0 ** -19).all()  # g^2 = 1.63
