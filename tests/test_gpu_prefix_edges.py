@@ -122,3 +122,16 @@ def test_workspace_of_the_prefix_alone(S, tails, Q):
     check(o, lse, tuple(to_np(x) for x in everything(t)), f"prefix {S}")
     with pytest.raises(RuntimeError, match="workspace"):
         t.run(ws=room[guard:guard + n - 1])
+
+
+@pytest.mark.parametrize("B,Q", [(31, 1), (32, 1), (33, 1), (11, 3), (8, 4), (147, 1), (148, 1), (149, 1), (1, 33)])
+@pytest.mark.parametrize("S,spread", [(0, 40), (600, 1), (300, 900), (2600, 2)])
+def test_row_counts_where_the_plan_changes(B, Q, S, spread):
+    """Rows that one warp plans and rows that the block does (32, 33), as many rows as blocks, one more; equal rows and
+    rows of unequal length, one of them seeing nothing."""
+    t = Batch(S, [(spread * ((7 * b) % 11)) // 10 for b in range(B)], 1, 16, 100 if S % 600 else 0, Q, seed=48)
+    if B > 2:
+        t.q_pos[B // 2] = -1
+    o, lse = t.run()
+    assert K().csa2_check(t.err) == 0
+    check(o, lse, tuple(to_np(x) for x in everything(t)), f"{B} x {Q} rows over {S}")
