@@ -354,7 +354,8 @@ def csa2_plan_v41():
 
 
 class DecodeStep:
-    """Descriptor of csa2_decode_step over caller-owned device tensors (marshalling only).
+    """Descriptor of csa2_decode_step over caller-owned device tensors (marshalling only).  Nothing in it is rotated: a
+    step with rotary positions is made of the single calls.
 
     plan: [(mode, source, cache)] per layer (mode: a MODE value or LAYER_SWA); caches: GlobalKVCache
     per cache id; max_entries: per cache.  Tensors are layer-major as csa2.h describes.
@@ -399,7 +400,9 @@ def csa2_rotary_table(rot_dim, base=10000.0, scaling="none", factor=1.0, origina
 class Rotary:
     """A rotation of 2 * len(step) dims of a head, from dim `first`: its device table of steps and descriptor.
 
-    Rotary.table(64, ..., device=..., first=448, layout="half") makes the steps with csa2_rotary_table.
+    Rotary.table(64, ..., device=..., first=448, layout="half") makes the steps with csa2_rotary_table.  The main and the
+    indexer values' rotations should share one: main = Rotary.table(64, first=448), index = Rotary(main.step, 64,
+    main.layout, main.scale); with two tables, even of equal content, csa2_pack_kv_rotary takes nearly twice the time.
     """
 
     def __init__(self, step, first=0, layout="interleaved", scale=1.0):

@@ -440,9 +440,11 @@ __global__ void __launch_bounds__(256) pack_kv_kernel(const T *__restrict__ lat_
 
 // The rotating pack of a chunk whose main and indexer values share one table of at most 32 pairs: a warp takes `run`
 // consecutive entries (lanes as in pack_kv_kernel; lane l turns pair l), so that a sine and cosine in fp64 serve 32 of them
-// (EntryAngle), and asks for the next entry's first token before it quantises this one.  Bound by instruction issue (about 440 a warp and
-// entry) and what of its latencies 24 warps an SM leave: 131288 bf16 tokens, r = 1, with the values stored, 82 us (71 % of
-// the copy rate; a sine and cosine per entry 162 us); 64000 fp32 tokens 49 us.  Blocks are as many as leave
+// (EntryAngle), and asks for the next entry's first token before it quantises this one.  Bound by its 442 instructions a warp and
+// entry, which fill 68 % of the issue slots, and by the latencies that 24 warps an SM leave uncovered (fixed ones, and the
+// turned values' way through shared memory): 131288 bf16 tokens, r = 1, with the values stored, 80 us (73 % of the copy
+// rate); 64000 fp32 tokens 50 us.  Other rotations (two tables, even of equal content, or more than 64 dims) are
+// pack_kv_kernel's: with two tables 136 us, with 128 turned dims 143, gated 426.  Blocks are as many as leave
 // registers enough: with 64 a thread, 32 warps an SM, a few spilled values made it 99 us (fp32, 80 a thread: 65 us).
 constexpr int64_t PACK_RUN = 64;  // entries that a warp takes at most
 template <typename T>

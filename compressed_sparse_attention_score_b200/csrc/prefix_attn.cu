@@ -24,11 +24,12 @@
 // below its maximum.  The sums are fp32 of the unrounded weights.
 //
 // What bounds it: a product of 128 x 64 x 16 reads 6 KB of shared memory (48.8 clocks; the tensor core would take 32), a
-// tile has 64 of them, and its 128 KB are written there too: 4150 clocks a tile, 4850 measured (2.75 us; 4.9 us where the
-// tile is dequantised in the block).  The rest is the softmax between a tile's products; TMEM and shared memory
-// hold one row's tile, so nothing else can run meanwhile.
-// Measured (whole call): 32 rows over 8192 shared entries 70 us, 96 over 4096 98 us, 16 over 65536 208 us (665
-// TFLOP/s), 13 over 2999 34 us, 2 over 96 21 us.
+// tile has 64 of them, and its 128 KB are written there too: 4150 clocks a tile, 4700 to 5000 measured where it is copied
+// (2.6 to 2.7 us at the 1.80 GHz that the SMs average in this kernel) and 9500 to 10000 where it is dequantised in the block
+// (5.4 us).  The rest is the softmax between a tile's products; TMEM and shared memory hold one row's tile, so nothing else
+// can run meanwhile.
+// Measured (whole call): 32 rows over 8192 shared entries 68 us, 96 over 4096 96 us, 16 over 65536 200 us (692
+// TFLOP/s), 13 over 2999 33 us, 2 over 96 21 us.
 #include <cuda_fp16.h>
 #include <string.h>
 
@@ -51,8 +52,9 @@ constexpr int PX_REG_SOFT = 128, PX_REG_ISSUE = 32;
 static_assert(PX_PROD * 96 + PX_SOFT * PX_REG_SOFT + 128 * PX_REG_ISSUE <= 96 * PX_THREADS,
               "the warpgroups' registers exceed the block's");
 // A shared prefix is dequantised ahead where at least this many rows have at least this many tiles of it in all (2.7 tiles a
-// block).  Measured, ahead against by every row: 16 rows over 8192 entries 51 / 66 us, 8 over 8192 44 / 48, 6 over 8192 44 / 45,
-// 4 over 32768 73 / 75; 16 over 2048 32 / 31, 4 over 8192 37 / 35, 2 over 32768 83 / 79.
+// block).  Measured, ahead against by every row (up to 100 own entries and a window of 128): 16 rows over 8192 entries
+// 43 / 60 us, 8 over 8192 39 / 43, 4 over 32768 60 / 66; 6 over 8192 38 / 39, 16 over 2048 31 / 29, 4 over 8192 35 / 33,
+// 2 over 32768 67 / 64.
 constexpr int PX_MIN_ROWS = 4, PX_MIN_SHARED = 400;
 constexpr int PX_MAX_CTAS = 160;             // workspace is sized for at most this many blocks
 constexpr float PX_LAG = 5.f, PX_BIAS = 5.f;
@@ -123,8 +125,8 @@ __device__ __forceinline__ RowKeys row_keys(const PrefixArgs &p, int row) {
 // A row of n tiles in at most `parts` parts: no part of fewer than two tiles (joining a partial row costs about what
 // a tile does); and the first tile of part i.
 __device__ __forceinline__ int part_count(int n, int parts) { return min((n + 1) / 2, parts); }
-// Dequantising a tile in the block costs about 7/4 of copying it (4.9 against 2.8 us), so parts are equal by that measure; the
-// row's first `shared` tiles are copied.
+// Dequantising a tile in the block costs twice what copying it does (see above); parts are equal with 7 : 4 for it, as all
+// the measured calls were split (2 : 1 was not tried).  The row's first `shared` tiles are copied.
 __device__ __forceinline__ int part_start(int n, int shared, int i, int parts) {
   const int m = part_count(n, parts);
   if (i >= m) return n;

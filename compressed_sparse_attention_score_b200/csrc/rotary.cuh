@@ -8,8 +8,8 @@ namespace csa2 {
 // modulo 2^64, which is modulo one turn, so the angle is exact at every position.
 __device__ __forceinline__ int64_t rotary_turn(uint64_t step, int64_t p) { return int64_t(step * uint64_t(p)); }
 
-// cos and sin in fp32: the turn rounded to fp32 (an angle error of at most 2^-24 pi) for the rotation of
-// bf16 and fp32 heads, whose own rounding is as coarse or coarser.
+// cos and sin in fp32, for the rotation of heads: the turn rounded to fp32, an angle error of at most 2^-24 pi.  That is
+// far below the rounding of bf16 heads; fp32 heads are off by up to 2^-21 of their pair's size with it.
 __device__ __forceinline__ float2 rotary_cs32(uint64_t step, int64_t p) {
   float c, s;
   sincospif(float(rotary_turn(step, p)) * 0x1p-63f, &s, &c);

@@ -99,7 +99,8 @@ typedef struct {
   int32_t batch;              /* sequences described by this cache */
   int32_t ratio;              /* tokens per entry, >= 1 */
   int32_t seq_stride;         /* contiguous layout: slots per sequence */
-  int32_t page_size;          /* paged layout: entries per page (power of two) */
+  int32_t page_size;          /* paged layout: entries per page (power of two; csa2_append_kv and
+                                 csa2_decode_step take any, the other entry points refuse them) */
   int32_t max_pages;          /* paged layout: page-table row length */
 } csa2_cache;
 
@@ -364,6 +365,9 @@ int32_t csa2_plan_v41(csa2_layer_plan *plan, int32_t max_layers, int32_t *cache_
  * attention; Reindex the same over the pool; Reuse and window-only layers: one attention
  * launch), on `stream` without synchronising or allocating (capturable in a CUDA graph).
  * Dense layers hold at most one segment (4096 entries).
+ * Nothing is rotated here: entries and window tokens are stored as csa2_append_kv and csa2_pack_swa
+ * store them.  A step with rotary positions is made of the single calls (csa2_rotate,
+ * csa2_append_kv_rotary, csa2_pack_swa_rotary, then csa2_sparse_attn or csa2_prefix_attn).
  */
 typedef struct {
   int32_t n_layers;
@@ -493,6 +497,8 @@ csa2_status csa2_rotate(const void *x, csa2_dtype x_dtype, int64_t x_token_strid
  *   value in some 2^20, and hardly ever a code); then quantised as csa2_pack_kv does.  An entry's
  *   angles follow from its number, the ratio and the rotations alone: its bytes are the same in a
  *   chunk of any size and when csa2_append_kv_rotary completes it.
+ *   Fastest without gates, with one table of at most 32 pairs: both rotations give the same step
+ *   pointer and rot_dim (a second table of equal content is another table), or one of them is NULL.
  *   pool_w as csa2_pack_kv, or gate_kv and gate_ix as csa2_pack_kv_gated (not both; all NULL: the mean).
  *   kv_hat [B][T/r][512], ix_hat [B][T/r][128] bf16 (optional, NULL: none) receive the values that
  *   the new entries' codes stand for, exactly (what attention will read back).
